@@ -1,4 +1,5 @@
-"""Build libkvx.so (the HIP library behind the C ABI in include/kvx.h) for gfx950, in-tree.
+"""Build libkvx.so (the HIP library behind the C ABI in include/kvx.h and include/kvx_attention.h)
+for gfx950, in-tree.
 
     python -m block_table_contiguous_amd.build          # compile
     python -m block_table_contiguous_amd.build --asm    # also keep the device assembly
@@ -17,11 +18,13 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkvx.so")
-SOURCES = ["kvx_api.hip", "kvx_kernels.hip", "kvx_signal.hip"]
+SOURCES = ["kvx_api.hip", "kvx_kernels.hip", "kvx_signal.hip"]  # the transfer path (include/kvx.h)
+# the calls that compute on a paged cache (include/kvx_attention.h)
+ATTENTION_SOURCES = ["kvx_attention_api.hip", "kvx_attention.hip", "kvx_rope.hip", "kvx_evict.hip"]
 ARCH = "gfx950"
 
-# Packed-FP32 instructions are disabled for all device code (the kernels do no float
-# arithmetic, but the flag keeps the compiler from ever forming them).
+# Packed-FP32 instructions are disabled for all device code: the copy kernels do no float
+# arithmetic, and in the attention kernels the flag keeps the compiler from ever forming them.
 HIP_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -42,13 +45,21 @@ def build(asm_dir: str | None = None, verbose: bool = False) -> str:
     objs = []
     tmp = os.path.join(PKG, "_build")
     os.makedirs(tmp, exist_ok=True)
-    for src in SOURCES:
+    sources = SOURCES + ATTENTION_SOURCES
+    jobs = []
+    for src in sources:  # one compiler process a source, at once
         obj = os.path.join(tmp, src.replace(".hip", ".o"))
         cmd = [cc, *HIP_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
+        jobs.append((cmd, subprocess.Popen(cmd)))
         objs.append(obj)
+    for _, job in jobs:
+        job.wait()
+    for cmd, job in jobs:
+        if job.returncode:
+            raise subprocess.CalledProcessError(job.returncode, cmd)
+    for src in sources:
         if asm_dir:
             os.makedirs(asm_dir, exist_ok=True)
             out = os.path.join(asm_dir, src.replace(".hip", f"-{ARCH}.s"))

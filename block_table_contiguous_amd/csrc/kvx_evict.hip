@@ -1,0 +1,223 @@
+// gfx950 kernels of kvx_evict_select and kvx_evict_compact.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kvx_attention_launch.h"
+#include "kvx_paged.h"
+
+namespace kvx {
+namespace {
+
+// --------------------------------------------------------------------------------------
+// selection
+// --------------------------------------------------------------------------------------
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelWaves = kSelThreads / 64;
+
+// Masses as integers of the same order: protected slots above NaN above +inf, -0 as 0.
+__device__ __forceinline__ uint32_t rank_of(float m) {
+  if (m != m) return 0xfffffffeu;
+  const uint32_t b = __builtin_bit_cast(uint32_t, m + 0.0f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// One workgroup a list. The rank of the last kept slot is found digit by digit from the top (a
+// histogram of 8 bits a round over the slots that agree with the digits found); then one ordered
+// pass writes the slots above it and the lowest ones that equal it.
+__global__ __launch_bounds__(kSelThreads) void select_kernel(SelectArgs a) {
+  __shared__ uint32_t hist[256];
+  __shared__ uint32_t waves_gt[kSelWaves], waves_eq[kSelWaves];
+  __shared__ uint32_t found[2];  // digit, slots still wanted among those that have it
+  const int r = blockIdx.x / a.num_heads, h = blockIdx.x - r * a.num_heads;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t c = a.context_lens[r];
+  const int64_t clamped = c < 0 ? 0 : c > a.width ? a.width : c;
+  if (c != clamped && tid == 0) raise(a.err, KVX_DEVERR_TABLE_RANGE);
+  const int n = (int)clamped, want_all = n < a.budget ? n : a.budget;
+  if (h == 0 && tid == 0) a.new_lens[r] = want_all;
+  int32_t* keep = a.keep + (int64_t)blockIdx.x * a.budget;
+  if (n <= a.budget) {
+    for (int64_t i = tid; i < a.budget; i += kSelThreads) keep[i] = i < n ? (int32_t)i : -1;
+    return;
+  }
+  const float* mass = a.mass + r * a.req_stride + h * a.head_stride;
+  const int last = n - a.recent;
+  auto rank_at = [&](int j) -> uint32_t {
+    return j < a.sink || j >= last ? 0xffffffffu : rank_of(mass[j]);
+  };
+  uint32_t prefix = 0, mask = 0, want = (uint32_t)want_all;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    if (tid < 256) hist[tid] = 0;
+    __syncthreads();
+    for (int j = tid; j < n; j += kSelThreads) {
+      const uint32_t k = rank_at(j);
+      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1u);
+    }
+    __syncthreads();
+    if (wave == 0) {  // lane l: bins 255-4l .. 252-4l, from the largest down
+      uint32_t b[4], sum = 0;
+      for (int i = 0; i < 4; ++i) sum += b[i] = hist[255 - 4 * lane - i];
+      uint32_t upto = sum;
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = __shfl_up(upto, d);
+        if (lane >= d) upto += o;
+      }
+      uint32_t before = upto - sum;
+      for (int i = 0; i < 4; ++i) {
+        if (before < want && want <= before + b[i]) {
+          found[0] = 255 - 4 * lane - i;
+          found[1] = want - before;
+        }
+        before += b[i];
+      }
+    }
+    __syncthreads();
+    prefix |= found[0] << shift;
+    mask |= 255u << shift;
+    want = found[1];
+    __syncthreads();
+  }
+  uint32_t base = 0, ties = want;  // slots written so far; equal slots still to write
+  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
+    const int j = j0 + tid;
+    const uint32_t k = j < n ? rank_at(j) : 0;
+    const bool gt = j < n && k > prefix, eq = j < n && k == prefix;
+    const uint64_t bg = __ballot(gt), be = __ballot(eq), under = (1ull << lane) - 1;
+    if (lane == 0) {
+      waves_gt[wave] = __popcll(bg);
+      waves_eq[wave] = __popcll(be);
+    }
+    __syncthreads();
+    uint32_t g = 0, e = 0, all_g = 0, all_e = 0;
+    for (int w = 0; w < kSelWaves; ++w) {
+      if (w < wave) g += waves_gt[w], e += waves_eq[w];
+      all_g += waves_gt[w], all_e += waves_eq[w];
+    }
+    g += __popcll(bg & under);
+    e += __popcll(be & under);
+    const uint32_t e_kept = e < ties ? e : ties;
+    if (gt || (eq && e < ties)) keep[base + g + e_kept] = j;
+    const uint32_t t = all_e < ties ? all_e : ties;
+    base += all_g + t;
+    ties -= t;
+    __syncthreads();
+  }
+}
+
+// --------------------------------------------------------------------------------------
+// moving
+// --------------------------------------------------------------------------------------
+
+constexpr int kMoveThreads = 256;
+constexpr int kMoveUnroll = 8;
+
+// A workgroup moves one column: the K or V rows of one KV head of one request, or one row of
+// masses, a tile of slots at a time: all its loads, then all its stores. An ascending list has
+// keep[i] >= i, so a slot is read in its own tile or an earlier one; with the tiles of a column in
+// one workgroup (grid.y = 1), in order and with a barrier between a tile's loads and its stores,
+// the move is right in place. Where source and destination differ, grid.y spreads the tiles.
+__global__ __launch_bounds__(kMoveThreads) void compact_kernel(CompactArgs a, BlockDiv div) {
+  const kvx_paged_cache& cache = a.cache;
+  const int columns = 2 * cache.num_kv_heads + (a.mass ? a.num_heads : 0);
+  const int r = blockIdx.x / columns, col = blockIdx.x - r * columns;
+  const int tid = threadIdx.x;
+  const bool in_place = a.src_table == a.dst_table;
+  int errs = 0;
+  if (col >= 2 * cache.num_kv_heads) {
+    const int h = col - 2 * cache.num_kv_heads;
+    const int32_t* keep = a.keep + ((int64_t)r * a.num_heads + h) * a.budget;
+    const float* in = a.mass + r * a.mass_req_stride + h * a.mass_head_stride;
+    float* out = a.mass_out + r * a.out_req_stride + h * a.out_head_stride;
+    const int64_t tile = kMoveThreads * kMoveUnroll;
+    for (int64_t t0 = blockIdx.y * tile; t0 < a.out_width; t0 += gridDim.y * tile) {
+      float v[kMoveUnroll];
+#pragma unroll
+      for (int u = 0; u < kMoveUnroll; ++u) {
+        const int64_t i = t0 + u * kMoveThreads + tid;
+        const int32_t k = i < a.budget && i < a.out_width ? keep[i] : -1;
+        v[u] = 0;
+        if (k >= 0 && k < i) errs |= KVX_DEVERR_OFFSETS;
+        else if (k >= a.mass_width) errs |= KVX_DEVERR_TABLE_RANGE;
+        else if (k >= 0) v[u] = in[k];
+      }
+      __builtin_amdgcn_s_waitcnt(0);  // the loads have landed in every wave before any store
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kMoveUnroll; ++u) {
+        const int64_t i = t0 + u * kMoveThreads + tid;
+        if (i < a.out_width) out[i] = v[u];
+      }
+    }
+  } else {
+    const int h = col >> 1;
+    const int64_t at = (col & 1) * cache.kv_stride_bytes + h * cache.head_stride_bytes;
+    const int list = h / (cache.num_kv_heads / a.num_heads);
+    const int32_t* keep = a.keep + ((int64_t)r * a.num_heads + list) * a.budget;
+    const int32_t* from = a.src_table + r * a.src_row;
+    const int32_t* to = a.dst_table + r * a.dst_row;
+    const uint32_t vecs = cache.head_dim / 8;
+    const int tile_rows = kMoveThreads * kMoveUnroll / vecs;
+    for (int64_t t0 = (int64_t)blockIdx.y * tile_rows; t0 < a.budget; t0 += (int64_t)gridDim.y * tile_rows) {
+      u32x4 v[kMoveUnroll];
+      char* dst[kMoveUnroll];
+#pragma unroll
+      for (int u = 0; u < kMoveUnroll; ++u) {
+        const uint32_t x = u * kMoveThreads + tid, row = x / vecs, c = x - row * vecs;
+        const int64_t i = t0 + row;
+        dst[u] = nullptr;
+        if ((int)row >= tile_rows || i >= a.budget) continue;
+        const int32_t k = keep[i];
+        if (k < 0) continue;
+        if (k < i) {
+          errs |= KVX_DEVERR_OFFSETS;
+          continue;
+        }
+        const int32_t sb = block_of(div, k), db = block_of(div, (int32_t)i);
+        if (sb >= a.src_cols || db >= a.dst_cols) {
+          errs |= KVX_DEVERR_TABLE_RANGE;
+          continue;
+        }
+        const int64_t s = from[sb], d = to[db];
+        if (s < 0 || s >= cache.num_blocks || d < 0 || d >= cache.num_blocks) {
+          errs |= KVX_DEVERR_BLOCK_RANGE;
+          continue;
+        }
+        if (in_place && k == i) continue;
+        const char* src = (const char*)cache.base + s * cache.block_stride_bytes +
+                          (int64_t)(k - sb * div.size) * cache.token_stride_bytes + at + c * 16;
+        dst[u] = (char*)cache.base + d * cache.block_stride_bytes +
+                 (int64_t)((int32_t)i - db * div.size) * cache.token_stride_bytes + at + c * 16;
+        v[u] = gload<u32x4>(src);
+      }
+      __builtin_amdgcn_s_waitcnt(0);  // the loads have landed in every wave before any store
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kMoveUnroll; ++u)
+        if (dst[u]) gstore(dst[u], v[u]);
+    }
+  }
+  if (errs) raise(a.err, errs);
+}
+
+}  // namespace
+
+hipError_t launch_evict_select(const SelectArgs& a, hipStream_t stream) {
+  select_kernel<<<dim3((unsigned)(a.num_reqs * a.num_heads)), dim3(kSelThreads), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_evict_compact(const CompactArgs& a, hipStream_t stream) {
+  const int columns = 2 * a.cache.num_kv_heads + (a.mass ? a.num_heads : 0);
+  const int tile_rows = kMoveThreads * kMoveUnroll / (a.cache.head_dim / 8);
+  int64_t tiles = 1;
+  if (a.src_table != a.dst_table) {
+    tiles = ((int64_t)a.budget + tile_rows - 1) / tile_rows;
+    if (tiles > 65535) tiles = 65535;
+  }
+  compact_kernel<<<dim3((unsigned)(a.num_reqs * columns), (unsigned)tiles), dim3(kMoveThreads), 0, stream>>>(
+      a, block_div(a.cache.block_size));
+  return hipGetLastError();
+}
+
+}  // namespace kvx

@@ -1,4 +1,4 @@
-"""Python binding of libkvx (include/kvx.h): argument marshalling only.
+"""Python binding of libkvx (include/kvx.h, include/kvx_attention.h): argument marshalling only.
 
 Each kvx_* function here takes torch tensors, checks that they are device tensors of the
 right dtype and contiguity, and passes their data pointers, sizes and the current HIP stream
@@ -40,11 +40,36 @@ NOALLOC_SLOTS = 16  # arrivals workspaces the library keeps per GPU for kvx_pack
 MAX_EXTENT_BYTES = 1 << 56  # largest byte extent one call may describe (KVX_MAX_EXTENT_BYTES)
 XFER_BYTES = 32  # sizeof(kvx_xfer)
 
+DTYPE_BF16, DTYPE_FP16 = 0, 1  # element types of the calls that compute (KVX_DTYPE_*)
+MAX_HEAD_DIM = 256
+MAX_AXES = 4
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 
-# name -> (restype, argtypes); mirrors include/kvx.h
+
+
+class PagedCache(ctypes.Structure):
+    """kvx_paged_cache: one layer's cache for the calls of kvx_attention.h (see paged_cache)."""
+
+    _fields_ = [("base", _P), ("num_blocks", _I64), ("block_stride_bytes", _I64), ("token_stride_bytes", _I64),
+                ("kv_stride_bytes", _I64), ("head_stride_bytes", _I64), ("block_size", _I32), ("num_kv_heads", _I32),
+                ("head_dim", _I32), ("dtype", _I32)]
+
+
+class Batch(ctypes.Structure):
+    """kvx_batch: the requests of one attention call."""
+
+    _fields_ = [("block_table", _P), ("q_offsets", _P), ("context_lens", _P), ("max_blocks_per_req", _I64),
+                ("bt_row_stride", _I64), ("num_tokens", _I64), ("max_query_len", _I64), ("max_context_len", _I64),
+                ("num_reqs", _I32)]
+
+
+_F32 = ctypes.c_float
+_CACHE, _BATCH = ctypes.POINTER(PagedCache), ctypes.POINTER(Batch)
+
+# name -> (restype, argtypes); mirrors include/kvx.h and include/kvx_attention.h
 SIGNATURES = {
     "kvx_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kvx_abi_version": (_I32, []),
@@ -65,6 +90,16 @@ SIGNATURES = {
                                               _P, _P, _P]),
     "kvx_pack_signal_noalloc": (ctypes.c_int, [_P, _I32, _I64, _I64, _P, _P, _I64, _P, _P, ctypes.c_uint64, _I32,
                                                _P, _P]),
+    "kvx_rope_and_cache": (ctypes.c_int, [_CACHE, _P, _I64, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _I32,
+                                          ctypes.POINTER(_I32), _P, _I32, _I32, _P, _P, _I64, _I64, _P, _P]),
+    "kvx_paged_attention": (ctypes.c_int, [_CACHE, _BATCH, _P, _I64, _I64, _I32, _F32, _I32, _I64, _P, _I64, _I64, _P,
+                                           _P, _I64, _P, _P]),
+    "kvx_paged_attention_workspace": (_I64, [_CACHE, _BATCH, _I32]),
+    "kvx_attention_mass": (ctypes.c_int, [_CACHE, _BATCH, _P, _I64, _I64, _I32, _F32, _I32, _I64, _P, _P, _I64, _I64,
+                                          _I64, _P, _P]),
+    "kvx_evict_select": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _I32, _P, _I64, _I64, _I64, _P, _P, _P, _P]),
+    "kvx_evict_compact": (ctypes.c_int, [_CACHE, _P, _I64, _I64, _P, _I64, _I64, _I32, _I32, _P, _I64, _P, _I64, _I64,
+                                         _I64, _P, _I64, _I64, _I64, _P, _P]),
 }
 
 
@@ -542,3 +577,275 @@ def _torch_int64():
     import torch
 
     return torch.int64
+
+
+# ---------------------------------------------------------------------------------------
+# calls that compute on a paged cache (include/kvx_attention.h)
+# ---------------------------------------------------------------------------------------
+
+def _step(t, dim: int) -> int:
+    """Stride of a dimension in elements; 0 where it has at most one entry and is never stepped."""
+    return t.stride(dim) if t.shape[dim] > 1 else 0
+
+
+def _dtype_code(t, name: str) -> int:
+    import torch
+
+    if t.dtype == torch.bfloat16:
+        return DTYPE_BF16
+    if t.dtype == torch.float16:
+        return DTYPE_FP16
+    raise TypeError(f"kvx: {name} must be bfloat16 or float16, got {t.dtype}")
+
+
+def _on_current_device(*tensors):
+    """Every tensor given lives on the current device, whose stream the call is enqueued on."""
+    import torch
+
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("kvx: tensors must live on the GPU")
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != here:
+            raise ValueError("kvx: every tensor must live on the current device")
+
+
+def paged_cache(kv_cache, layout: str = "blocks_tokens_kv") -> PagedCache:
+    """A 5-D cache tensor (one of cache_strides' layouts, any strides whose last dimension is
+    dense) as the struct that the calls below take. They make it from the tensor themselves; a
+    caller that makes the same call many times can make it once and pass it with the tensor kept
+    alive."""
+    if kv_cache.dim() != 5 or kv_cache.shape[{"blocks_tokens_kv": 2, "blocks_kv_tokens": 1}.get(layout, 0)] != 2:
+        raise ValueError("kvx: kv_cache must be a 5-D cache tensor of the given layout")
+    code = _dtype_code(kv_cache, "kv_cache")
+    nb, bs, block, token, kv = cache_strides(kv_cache, layout)
+    if kv_cache.shape[4] > 1 and kv_cache.stride(4) != 1:
+        raise ValueError("kvx: the last dimension of kv_cache must be dense")
+    c = PagedCache(kv_cache.data_ptr(), nb, block if nb > 1 else 0, token if bs > 1 else 0, kv,
+                   _step(kv_cache, 3) * 2, bs, kv_cache.shape[3], kv_cache.shape[4], code)
+    c.tensor = kv_cache
+    return c
+
+
+def _cache(kv_cache, layout) -> PagedCache:
+    return kv_cache if isinstance(kv_cache, PagedCache) else paged_cache(kv_cache, layout)
+
+
+def _want_heads(t, tokens, heads, cache: PagedCache, name: str):
+    """A [tokens][heads][head_dim] tensor of the cache's element type, its last dimension dense
+    (heads None: any number)."""
+    if t.dim() != 3 or t.shape[0] != tokens or (heads is not None and t.shape[1] != heads) \
+            or t.shape[2] != cache.head_dim:
+        raise ValueError(f"kvx: {name} must be [num_tokens][heads][head_dim]")
+    if _dtype_code(t, name) != cache.dtype:
+        raise TypeError(f"kvx: {name} and kv_cache must have the same element type")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"kvx: the last dimension of {name} must be dense")
+
+
+def _want_table(t, name="block_table"):
+    import torch
+
+    if t.dtype != torch.int32 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"kvx: {name} must be a row-major int32 [num_reqs][width] tensor")
+
+
+def _row_stride(table) -> int:
+    return table.stride(0) if table.shape[0] > 1 else table.shape[1]
+
+
+def _want_lists(t, name: str, reqs: int, heads: Optional[int], width: Optional[int] = None):
+    """Float32 [num_reqs][heads][width], its last dimension dense."""
+    import torch
+
+    if t.dtype != torch.float32:
+        raise TypeError(f"kvx: {name} must be torch.float32, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != reqs or (heads is not None and t.shape[1] != heads) \
+            or (width is not None and t.shape[2] != width):
+        raise ValueError(f"kvx: {name} must be [num_reqs][heads][width]")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"kvx: the last dimension of {name} must be dense")
+
+
+def kvx_rope_and_cache(query, key, value, positions, inv_freq, pair_axis: Sequence[int], slot_mapping, kv_cache,
+                       query_out, layout: str = "blocks_tokens_kv", interleaved: bool = False, err_flag=None,
+                       stream=None):
+    """Rotate query into query_out and key into the cache by positions ([num_axes][num_tokens]),
+    pair i by positions[pair_axis[i]] * inv_freq[i], and write the rotated K row and the V row of
+    every token through its slot (negative slot = no row). query and query_out may be None."""
+    import torch
+
+    c = _cache(kv_cache, layout)
+    _want(slot_mapping, torch.int64, "slot_mapping")
+    _want(positions, torch.int64, "positions")
+    _want(inv_freq, torch.float32, "inv_freq")
+    T = slot_mapping.numel()
+    if positions.dim() != 2 or positions.shape[1] != T:
+        raise ValueError("kvx: positions must be [num_axes][num_tokens]")
+    pairs = len(pair_axis)
+    if inv_freq.numel() != pairs:
+        raise ValueError("kvx: pair_axis and inv_freq need one entry a pair")
+    if (query is None) != (query_out is None):
+        raise ValueError("kvx: query and query_out go together")
+    _want_heads(key, T, c.num_kv_heads, c, "key")
+    _want_heads(value, T, c.num_kv_heads, c, "value")
+    heads = 0
+    if query is not None:
+        _want_heads(query, T, None, c, "query")
+        heads = query.shape[1]
+        _want_heads(query_out, T, heads, c, "query_out")
+    _on_current_device(query, key, value, positions, inv_freq, slot_mapping, getattr(c, "tensor", None), query_out,
+                       err_flag)
+    q, o = query if query is not None else key, query_out if query is not None else key
+    st = _F["kvx_rope_and_cache"](
+        ctypes.byref(c), _ptr(query), _step(q, 0) * 2, _step(q, 1) * 2, heads, _ptr(key), _step(key, 0) * 2,
+        _step(key, 1) * 2, _ptr(value), _step(value, 0) * 2, _step(value, 1) * 2, T, _ptr(positions),
+        positions.shape[0], (_I32 * max(pairs, 1))(*pair_axis), _ptr(inv_freq), 2 * pairs, int(interleaved),
+        _ptr(slot_mapping), _ptr(query_out), _step(o, 0) * 2, _step(o, 1) * 2, _ptr(err_flag), _stream(stream))
+    _check("kvx_rope_and_cache", st)
+
+
+def _batch(query, c: PagedCache, block_table, q_offsets, context_lens, max_query_len, max_context_len) -> Batch:
+    import torch
+
+    T, R = query.shape[0], context_lens.numel()
+    _want_heads(query, T, None, c, "query")
+    if query.shape[1] == 0 or query.shape[1] % c.num_kv_heads:
+        raise ValueError("kvx: the query heads must be a multiple of the KV heads")
+    _want_table(block_table)
+    _want(q_offsets, torch.int64, "q_offsets")
+    _want(context_lens, torch.int64, "context_lens")
+    if block_table.shape[0] != R or q_offsets.numel() != R + 1:
+        raise ValueError("kvx: block_table needs a row a request and q_offsets num_reqs + 1 entries")
+    width = block_table.shape[1]
+    # plain addresses: _on_current_device checks the tensors before the call
+    return Batch(block_table.data_ptr(), q_offsets.data_ptr(), context_lens.data_ptr(), width,
+                 _row_stride(block_table), T, T if max_query_len is None else int(max_query_len),
+                 width * c.block_size if max_context_len is None else int(max_context_len), R)
+
+
+def attention_workspace_bytes(query, kv_cache, num_reqs: int, max_query_len: int, max_context_len: int,
+                              layout: str = "blocks_tokens_kv") -> int:
+    """Bytes of workspace with which kvx_paged_attention splits such a batch as far as pays."""
+    c = _cache(kv_cache, layout)
+    b = Batch(None, None, None, 0, 0, query.shape[0], int(max_query_len), int(max_context_len), int(num_reqs))
+    n = _F["kvx_paged_attention_workspace"](ctypes.byref(c), ctypes.byref(b), query.shape[1])
+    if n < 0:
+        raise ValueError("kvx: kvx_paged_attention does not take a batch of these sizes")
+    return int(n)
+
+
+def new_attention_workspace(query, kv_cache, num_reqs: int, max_query_len: int, max_context_len: int,
+                            layout: str = "blocks_tokens_kv"):
+    """A workspace of attention_workspace_bytes (one per concurrent stream or captured graph)."""
+    import torch
+
+    n = attention_workspace_bytes(query, kv_cache, num_reqs, max_query_len, max_context_len, layout)
+    return torch.empty(n, dtype=torch.uint8, device=query.device)
+
+
+def kvx_paged_attention(query, kv_cache, block_table, q_offsets, context_lens, out, lse=None,
+                        scale: Optional[float] = None, causal: bool = True, window: int = 0,
+                        max_query_len: Optional[int] = None, max_context_len: Optional[int] = None, workspace=None,
+                        layout: str = "blocks_tokens_kv", err_flag=None, stream=None):
+    """Attention of each request's new tokens (rows q_offsets[r] .. q_offsets[r+1]-1 of query,
+    [num_tokens][heads][head_dim]) over its paged cache of context_lens[r] slots, into out and,
+    if given, lse (float32 [num_tokens][heads]). scale defaults to head_dim ** -0.5; max_query_len
+    and max_context_len only choose the launch shape."""
+    import torch
+
+    c = _cache(kv_cache, layout)
+    b = _batch(query, c, block_table, q_offsets, context_lens, max_query_len, max_context_len)
+    heads = query.shape[1]
+    _want_heads(out, query.shape[0], heads, c, "out")
+    if lse is not None:
+        _want(lse, torch.float32, "lse")
+        if lse.shape != query.shape[:2]:
+            raise ValueError("kvx: lse must be [num_tokens][heads]")
+    nbytes = 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("kvx: workspace must be contiguous")
+        nbytes = workspace.numel() * workspace.element_size()
+    _on_current_device(query, getattr(c, "tensor", None), block_table, q_offsets, context_lens, out, lse, workspace,
+                       err_flag)
+    st = _F["kvx_paged_attention"](
+        ctypes.byref(c), ctypes.byref(b), _ptr(query), _step(query, 0) * 2, _step(query, 1) * 2, heads,
+        c.head_dim ** -0.5 if scale is None else float(scale), int(causal), int(window), _ptr(out), _step(out, 0) * 2,
+        _step(out, 1) * 2, _ptr(lse), _ptr(workspace), nbytes, _ptr(err_flag), _stream(stream))
+    _check("kvx_paged_attention", st)
+
+
+def kvx_attention_mass(query, kv_cache, block_table, q_offsets, context_lens, lse, mass,
+                       scale: Optional[float] = None, causal: bool = True, window: int = 0,
+                       max_query_len: Optional[int] = None, max_context_len: Optional[int] = None,
+                       layout: str = "blocks_tokens_kv", err_flag=None, stream=None):
+    """Add to mass (float32 [num_reqs][num_kv_heads][width]) the attention weight that the batch's
+    queries give to every cached token, summed over the query heads of each KV head; lse is
+    kvx_paged_attention's."""
+    import torch
+
+    c = _cache(kv_cache, layout)
+    b = _batch(query, c, block_table, q_offsets, context_lens, max_query_len, max_context_len)
+    heads = query.shape[1]
+    _want(lse, torch.float32, "lse")
+    if lse.shape != query.shape[:2]:
+        raise ValueError("kvx: lse must be [num_tokens][heads]")
+    _want_lists(mass, "mass", b.num_reqs, c.num_kv_heads)
+    _on_current_device(query, getattr(c, "tensor", None), block_table, q_offsets, context_lens, lse, mass, err_flag)
+    st = _F["kvx_attention_mass"](
+        ctypes.byref(c), ctypes.byref(b), _ptr(query), _step(query, 0) * 2, _step(query, 1) * 2, heads,
+        c.head_dim ** -0.5 if scale is None else float(scale), int(causal), int(window), _ptr(lse), _ptr(mass),
+        _step(mass, 0), _step(mass, 1), mass.shape[2], _ptr(err_flag), _stream(stream))
+    _check("kvx_attention_mass", st)
+
+
+def kvx_evict_select(mass, context_lens, budget: int, sink: int, recent: int, keep, new_lens, err_flag=None,
+                     stream=None):
+    """Per request and head of mass ([num_reqs][heads][width]): the slots that stay, ascending and
+    then -1, into keep (int32 [num_reqs][heads][budget]); min(context, budget) into new_lens."""
+    import torch
+
+    _want(context_lens, torch.int64, "context_lens")
+    _want(keep, torch.int32, "keep")
+    _want(new_lens, torch.int64, "new_lens")
+    R = context_lens.numel()
+    _want_lists(mass, "mass", R, None)
+    if keep.shape != (R, mass.shape[1], int(budget)) or new_lens.numel() != R:
+        raise ValueError("kvx: keep must be [num_reqs][heads][budget] and new_lens [num_reqs]")
+    _on_current_device(mass, context_lens, keep, new_lens, err_flag)
+    st = _F["kvx_evict_select"](_ptr(mass), _step(mass, 0), _step(mass, 1), mass.shape[2], R, mass.shape[1],
+                                _ptr(context_lens), int(budget), int(sink), int(recent), _ptr(keep), _ptr(new_lens),
+                                _ptr(err_flag), _stream(stream))
+    _check("kvx_evict_select", st)
+
+
+def kvx_evict_compact(kv_cache, block_table, dst_block_table, keep, mass=None, mass_out=None,
+                      layout: str = "blocks_tokens_kv", err_flag=None, stream=None):
+    """Move the kept slots' K and V rows (and masses) together, slot keep[r][h][i] to slot i of
+    dst_block_table: block_table itself for a move in place, else a table of other blocks."""
+    import torch
+
+    c = _cache(kv_cache, layout)
+    _want_table(block_table)
+    _want_table(dst_block_table, "dst_block_table")
+    _want(keep, torch.int32, "keep")
+    R = block_table.shape[0]
+    if keep.dim() != 3 or keep.shape[0] != R or dst_block_table.shape[0] != R:
+        raise ValueError("kvx: keep must be [num_reqs][heads][budget], with a row of both tables a request")
+    if keep.shape[1] == 0 or c.num_kv_heads % keep.shape[1]:
+        raise ValueError("kvx: the KV heads must be a multiple of the heads that chose")
+    if (mass is None) != (mass_out is None):
+        raise ValueError("kvx: mass and mass_out go together")
+    m = (0, 0, 0, 0, 0, 0)
+    if mass is not None:
+        _want_lists(mass, "mass", R, keep.shape[1])
+        _want_lists(mass_out, "mass_out", R, keep.shape[1])
+        m = (_step(mass, 0), _step(mass, 1), mass.shape[2], _step(mass_out, 0), _step(mass_out, 1), mass_out.shape[2])
+    _on_current_device(getattr(c, "tensor", None), block_table, dst_block_table, keep, mass, mass_out, err_flag)
+    st = _F["kvx_evict_compact"](
+        ctypes.byref(c), _ptr(block_table), block_table.shape[1], _row_stride(block_table), _ptr(dst_block_table),
+        dst_block_table.shape[1], _row_stride(dst_block_table), R, keep.shape[1], _ptr(keep), keep.shape[2],
+        _ptr(mass), m[0], m[1], m[2], _ptr(mass_out), m[3], m[4], m[5], _ptr(err_flag), _stream(stream))
+    _check("kvx_evict_compact", st)
