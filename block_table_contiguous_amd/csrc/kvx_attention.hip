@@ -9,91 +9,527 @@ namespace kvx {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
 
-// A token of the batch: its request, and the slots [lo, hi) it sees.
-struct Token {
-  int32_t r, lo, hi;
-  bool used;
+// --------------------------------------------------------------------------------------
+// which rows a workgroup computes
+// --------------------------------------------------------------------------------------
+
+// A query row of request r is one (token, head of the KV head's group) pair, token by token, so a
+// tile of rows shares its K and V whatever the number of heads in a group. The tiles of all
+// requests are numbered without any sum over the requests: request r's begin at
+// floor(first row / ROWS) + r, which leaves it at least the tiles it needs and at most one spare.
+struct Rows {
+  int32_t r;         // the request
+  int32_t context;   // its slots
+  int32_t tokens;    // its new tokens
+  int32_t tile;      // index of the tile in the request
+  int64_t q0;        // its first query row
 };
 
-__device__ __forceinline__ int32_t context_of(const AttendArgs& a, int r, int32_t* errs) {
-  const int64_t c = a.batch.context_lens[r], cap = a.batch.max_blocks_per_req * a.cache.block_size;
-  const int64_t x = c < 0 ? 0 : c > cap ? cap : c;
-  if (x != c) *errs |= KVX_DEVERR_TABLE_RANGE;
-  return (int32_t)x;
+__device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) {
+  return x < lo ? lo : x > hi ? hi : x;
 }
 
-// One workgroup of a launch looks every request's offsets over.
-__device__ void check_offsets(const AttendArgs& a, int tid, int threads) {
+// One workgroup of a launch looks every request's offsets and contexts over.
+__device__ void check_batch(const AttendArgs& a, int64_t cap, int tid, int threads) {
+  int errs = 0;
   for (int r = tid; r < a.batch.num_reqs; r += threads) {
-    const int64_t b = a.batch.q_offsets[r], e = a.batch.q_offsets[r + 1];
-    if (b < 0 || e < b || e > a.batch.num_tokens) raise(a.err, KVX_DEVERR_OFFSETS);
+    const int64_t b = a.batch.q_offsets[r], e = a.batch.q_offsets[r + 1], c = a.batch.context_lens[r];
+    if (b < 0 || e < b || e > a.batch.num_tokens) errs |= KVX_DEVERR_OFFSETS;
+    if (c < 0 || c > cap) errs |= KVX_DEVERR_TABLE_RANGE;
   }
-}
-
-__device__ Token token_of(const AttendArgs& a, int64_t t, int32_t* errs) {
-  int lo = 0, hi = a.batch.num_reqs;  // the last request that starts at or before t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.batch.q_offsets[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  const int64_t b = a.batch.q_offsets[lo], e = a.batch.q_offsets[lo + 1];
-  Token k = {lo, 0, 0, t >= b && t < e};
-  if (!k.used) return k;
-  const int32_t c = context_of(a, lo, errs);
-  const int64_t last = a.causal ? (int64_t)c - (e - t) : (int64_t)c - 1;
-  k.hi = (int32_t)(last + 1 < 0 ? 0 : last + 1);
-  const int64_t first = last - a.window + 1;
-  k.lo = (int32_t)(first < 0 ? 0 : first);
-  return k;
-}
-
-// One wavefront a query row, a slot at a time.
-template <class E>
-__global__ __launch_bounds__(64) void attend_simple(AttendArgs a, BlockDiv div) {
-  const int64_t t = blockIdx.x / a.num_heads;
-  const int h = blockIdx.x - t * a.num_heads, lane = threadIdx.x;
-  int32_t errs = 0;
-  if (blockIdx.x == 0) check_offsets(a, lane, 64);
-  const Token k = token_of(a, t, &errs);
-  if (!k.used) return;
-  const int g = h / (a.num_heads / a.cache.num_kv_heads), vecs = a.cache.head_dim / 8;
-  f32x8 q = {}, o = {};
-  if (lane < vecs)
-    q = widen<E>(gload<u32x4>(a.query.base + t * a.query.token_stride + h * a.query.head_stride + lane * 16));
-  float m = -INFINITY, l = 0;
-  for (int j = k.lo; j < k.hi; ++j) {
-    const int b = block_of(div, j);
-    const int64_t id = a.batch.block_table[k.r * a.batch.bt_row_stride + b];
-    if (id < 0 || id >= a.cache.num_blocks) {
-      errs |= KVX_DEVERR_BLOCK_RANGE;
-      continue;
-    }
-    const char* row = (const char*)a.cache.base + id * a.cache.block_stride_bytes +
-                      (int64_t)(j - b * div.size) * a.cache.token_stride_bytes + g * a.cache.head_stride_bytes;
-    float s = 0;
-    f32x8 v = {};
-    if (lane < vecs) {
-      const f32x8 kk = widen<E>(gload<u32x4>(row + lane * 16));
-      v = widen<E>(gload<u32x4>(row + a.cache.kv_stride_bytes + lane * 16));
-      for (int i = 0; i < 8; ++i) s += q[i] * kk[i];
-    }
-    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-    s *= a.scale * kLog2e;
-    const float top = fmaxf(m, s), base = top == -INFINITY ? 0 : top;
-    const float p = exp2f(s - base), keep = exp2f(m - base);
-    l = l * keep + p;
-    for (int i = 0; i < 8; ++i) o[i] = o[i] * keep + p * v[i];
-    m = top;
-  }
-  const float inv = l == 0 ? 0 : 1 / l;
-  if (lane < vecs) {
-    for (int i = 0; i < 8; ++i) o[i] = l == 0 ? 0 : o[i] * inv;
-    gstore((char*)a.out.base + t * a.out.token_stride + h * a.out.head_stride + lane * 16, narrow<E>(o));
-  }
-  if (a.lse && lane == 0) a.lse[t * a.num_heads + h] = l == 0 ? -INFINITY : (m + log2f(l)) / kLog2e;
   if (errs) raise(a.err, errs);
+}
+
+// The request of a tile: a 64-way search over the offsets, one probe a lane and round (one round
+// up to 64 requests). All lanes get the same answer; whatever the offsets hold, r is a request.
+template <int ROWS>
+__device__ __forceinline__ Rows find_rows(const AttendArgs& a, int32_t tile, int group, int64_t cap, int lane) {
+  int lo = 0, len = a.batch.num_reqs;
+  int64_t begin, end, context;
+  for (;;) {
+    const int step = (len + 63) / 64;
+    const int i = lane * step < len ? lo + lane * step : lo;
+    begin = clamp64(a.batch.q_offsets[i], 0, a.batch.num_tokens);
+    end = a.batch.q_offsets[i + 1];
+    context = a.batch.context_lens[i];
+    const bool at = lane * step < len && begin * group / ROWS + i <= tile;
+    const int hit = __popcll(__ballot(at));
+    const int pick = hit ? hit - 1 : 0;
+    if (step == 1) {
+      begin = __shfl(begin, pick);
+      end = __shfl(end, pick);
+      context = __shfl(context, pick);
+      lo += pick;
+      break;
+    }
+    lo += pick * step;
+    len = len - pick * step < step ? len - pick * step : step;
+  }
+  Rows x;
+  x.r = __builtin_amdgcn_readfirstlane(lo);
+  x.q0 = begin;
+  x.tokens = (int32_t)(clamp64(end, begin, a.batch.num_tokens) - begin);
+  x.context = a.cache.num_blocks > 0 ? (int32_t)clamp64(context, 0, cap) : 0;
+  x.tile = tile - (int32_t)(begin * group / ROWS + lo);
+  x.tokens = __builtin_amdgcn_readfirstlane(x.tokens);
+  x.context = __builtin_amdgcn_readfirstlane(x.context);
+  x.tile = __builtin_amdgcn_readfirstlane(x.tile);
+  return x;
+}
+
+// The slots [lo, hi) that new token i of a request sees.
+__device__ __forceinline__ int2 sees(const AttendArgs& a, const Rows& x, int token) {
+  const int64_t hi = a.causal ? (int64_t)x.context - x.tokens + token + 1 : (int64_t)x.context;
+  const int64_t lo = hi - a.window;
+  return {(int)(lo < 0 ? 0 : lo), (int)(hi < 0 ? 0 : hi)};
+}
+
+// --------------------------------------------------------------------------------------
+// matrix pieces
+// --------------------------------------------------------------------------------------
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+#define KVX_LDS __attribute__((address_space(3)))
+
+__device__ __forceinline__ f32x16 mfma(Bf16, u32x4 a, u32x4 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(Bf16::V8, a), __builtin_bit_cast(Bf16::V8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma(Fp16, u32x4 a, u32x4 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(Fp16::V8, a), __builtin_bit_cast(Fp16::V8, b), c, 0, 0, 0);
+}
+
+// In the 32x32x16 products lane l holds column (or row) l % 32 and, with hf = l / 32, elements
+// 8 hf .. 8 hf + 7 of the summed dimension; result register i of lane l is row 8 (i / 4) + 4 hf + i % 4,
+// column l % 32.
+
+// max or sum over the two lanes l and l ^ 32
+__device__ __forceinline__ float other_half(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+  return __builtin_bit_cast(float, (threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+template <class E>
+__device__ __forceinline__ bool non_finite(u32x4 v) {
+  constexpr uint32_t exp = sizeof(E) && __is_same(E, Bf16) ? 0x7f80u : 0x7c00u;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad |= (v[i] & exp) == exp || ((v[i] >> 16) & exp) == exp;
+  return bad;
+}
+
+// Barrier for data passed through LDS: global loads stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// --------------------------------------------------------------------------------------
+// attention
+// --------------------------------------------------------------------------------------
+
+struct Split {
+  int32_t count, tiles, kv_heads;  // parts a context is cut into; row tiles
+  float* lse;                      // [count][rows], base 2; null where count == 1
+  float* acc;                      // [count][rows][head_dim]
+  int64_t rows;
+};
+
+// One pass over the slots with a running maximum and sum. Scores are computed transposed, S^T = K Q^T, so that a lane
+// holds one query row and 16 slots of each 32: the row's maximum and sum need one exchange between two
+// lanes, and the weights are already where O^T += V^T P^T takes them, because the summed dimension may be
+// numbered in any order: V is read from LDS with the transposing load, four slots a lane, in the order in
+// which the score registers hold them. DP is head_dim padded to 64, 128 or 256.
+//   KEYS = false: the four wavefronts hold 32 rows each and share every 64 slots staged in LDS.
+//   KEYS = true (up to 32 rows): they hold the same rows and 32 slots each of every 128, meet
+//     only at the end, and need no barrier before it: bound by the bytes of K and V.
+// K and V go from memory to registers one tile ahead and then to LDS, 16-byte pieces XOR-swizzled by
+// slot so that the reads of 16 rows (K), or of 4 slots x 64 bytes (V), fall on different banks.
+template <class E, int DP, bool KEYS>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendArgs a, BlockDiv div, Split sp) {
+  constexpr int ROWS = KEYS ? 32 : 128, BN = KEYS ? 128 : 64, KW = BN / 4;
+  constexpr int VPR = DP / 8, RPI = 64 / VPR, NI = KW / RPI;
+  constexpr int KT = KEYS ? 1 : 2, KSTEPS = DP / 16, DT = DP / 32;
+  __shared__ __align__(16) char smem[2 * BN * DP * 2 + BN];
+  char* const sk = smem;
+  char* const sv = smem + BN * DP * 2;
+  uint8_t* const flags = (uint8_t*)(smem + 2 * BN * DP * 2);
+
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 31, hf = lane >> 5;
+  const int group = a.num_heads / a.cache.num_kv_heads, vecs = a.cache.head_dim / 8;
+  const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size;
+  const int g = blockIdx.y, split = blockIdx.z;
+  if (blockIdx.x == 0 && g == 0 && split == 0) check_batch(a, cap, tid, 256);
+  const Rows x = find_rows<ROWS>(a, sp.tiles - 1 - blockIdx.x, group, cap, lane);
+  const int row0 = x.tile * ROWS, rows = x.tokens * group;
+  if (row0 >= rows) return;
+
+  // this lane's row, what it sees, and what any row of the workgroup sees
+  const int row = row0 + (KEYS ? 0 : w * 32) + n;
+  const bool used = row < rows;
+  const int token = used ? row / group : 0, head = g * group + (used ? row - token * group : 0);
+  const int64_t q_row = x.q0 + token;
+  int2 see = sees(a, x, token);
+  if (!used) see = {0, 0};
+  const int last_row = row0 + ROWS < rows ? row0 + ROWS - 1 : rows - 1;
+  const int2 first = sees(a, x, row0 / group), last = sees(a, x, last_row / group);
+  const int kend = last.y;
+  const int t_first = first.x / BN, t_all = (kend + BN - 1) / BN - t_first;
+  int tb = t_first, te = t_first + (t_all > 0 ? t_all : 0);
+  if (sp.count > 1) {
+    tb = t_first + (int)((int64_t)(te - t_first) * split / sp.count);
+    te = t_first + (int)((int64_t)(te - t_first) * (split + 1) / sp.count);
+  }
+
+  // Q: lane n's row, eight elements a step
+  u32x4 q[KSTEPS];
+  {
+    const char* p = a.query.base + q_row * a.query.token_stride + head * a.query.head_stride;
+#pragma unroll
+    for (int s = 0; s < KSTEPS; ++s) {
+      q[s] = u32x4{0, 0, 0, 0};
+      if (used && 2 * s + hf < vecs) q[s] = gload<u32x4>(p + (2 * s + hf) * 16);
+    }
+  }
+
+  const int c = lane % VPR, sub = lane / VPR;  // the 16-byte piece and row this lane stages
+  const char* const kbase = (const char*)a.cache.base + g * a.cache.head_stride_bytes + (c < vecs ? c : 0) * 16;
+  const int32_t* const table = a.batch.block_table + x.r * a.batch.bt_row_stride;
+  const int cols = (int)a.batch.max_blocks_per_req;
+  auto k_swz = [](int r) { return VPR == 8 ? (r >> 1) & 7 : r & 15; };
+  auto v_swz = [](int r) { return VPR == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; };
+  if (vecs < VPR && c >= vecs) {  // the padding of every row is zero, once
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = w * KW + i * RPI + sub;
+      *(u32x4*)(sk + (r * VPR + (c ^ k_swz(r))) * 16) = u32x4{0, 0, 0, 0};
+      *(u32x4*)(sv + (r * VPR + (c ^ v_swz(r))) * 16) = u32x4{0, 0, 0, 0};
+    }
+  }
+
+  f32x16 acc[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) acc[d] = f32x16{};
+  float m = -INFINITY, l = 0;
+  const float c1 = a.scale * kLog2e;
+  int errs = 0;
+
+  // staging: lane l looks up slot l % KW of the wavefront's share of a tile
+  auto load_id = [&](int t) -> int32_t {
+    const int b = block_of(div, t * BN + w * KW + lane % KW);
+    return gload<int32_t>(table + (b < cols ? b : cols - 1));
+  };
+  u32x4 rk[NI], rv[NI];
+  uint64_t ok_mask = 0;
+  auto fetch = [&](int t, int32_t id) {
+    const int j = t * BN + w * KW + lane % KW;
+    const bool in = j < kend, ok = in && (uint32_t)id < (uint64_t)a.cache.num_blocks;
+    if (in && !ok) errs |= KVX_DEVERR_BLOCK_RANGE;
+    // a slot that is not there is read from the cache's first row and then set to zero
+    const int64_t off = ok ? id * a.cache.block_stride_bytes +
+                                 (int64_t)(j - block_of(div, j) * div.size) * a.cache.token_stride_bytes
+                           : 0;
+    ok_mask = __ballot(ok);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const char* p = kbase + __shfl(off, i * RPI + sub);
+      rk[i] = gload<u32x4>(p);
+      rv[i] = gload<u32x4>(p + a.cache.kv_stride_bytes);
+    }
+  };
+
+  int32_t id = 0;
+  if (tb < te) {
+    fetch(tb, load_id(tb));
+    id = load_id(tb + 1);
+  }
+  for (int t = tb; t < te; ++t) {
+    const int k0 = t * BN;
+    // every row sees every slot of an inner tile
+    const bool inner = k0 >= last.x && k0 + BN <= first.y;
+    if (lane < KW) flags[w * KW + lane] = (ok_mask >> lane) & 1;
+    if (~ok_mask) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if (!((ok_mask >> (i * RPI + sub)) & 1)) rk[i] = rv[i] = u32x4{0, 0, 0, 0};
+    }
+    if (!inner) {
+      // A weight of zero times a NaN or infinity is NaN: rows of V that hold one are left out of the
+      // products and added below for the query rows that see them.
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const uint64_t bad = __ballot(c < vecs && non_finite<E>(rv[i]));
+        if (VPR == 64 ? bad : (bad >> (sub * VPR)) & ((1ull << (VPR & 63)) - 1)) {
+          rv[i] = u32x4{0, 0, 0, 0};
+          if (c == 0) flags[w * KW + i * RPI + sub] = 3;
+        }
+      }
+    }
+    if (c < vecs) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = w * KW + i * RPI + sub;
+        *(u32x4*)(sk + (r * VPR + (c ^ k_swz(r))) * 16) = rk[i];
+        *(u32x4*)(sv + (r * VPR + (c ^ v_swz(r))) * 16) = rv[i];
+      }
+    }
+    if constexpr (KEYS) __builtin_amdgcn_wave_barrier();
+    else lds_barrier();
+    if (t + 1 < te) {
+      fetch(t + 1, id);
+      id = load_id(t + 2);
+    }
+
+    const int kw = KEYS ? w * KW : 0;  // first slot of the tile that this wavefront computes
+    const uint8_t flag = flags[kw + (lane & (KT * 32 - 1))];
+    // one bit a slot of this wavefront; with KEYS its 32 slots are read twice
+    const uint64_t there = __ballot(flag & 1), skipped = __ballot((flag & 2) && lane < KT * 32);
+    f32x16 s[KT];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      s[kt] = f32x16{};
+      const int r = kw + kt * 32 + n;
+#pragma unroll
+      for (int st = 0; st < KSTEPS; ++st)
+        s[kt] = mfma(E(), *(const u32x4*)(sk + (r * VPR + ((2 * st + hf) ^ k_swz(r))) * 16), q[st], s[kt]);
+    }
+    if (!inner || ~there) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int o = kt * 32 + 8 * (i / 4) + 4 * hf + i % 4, j = k0 + kw + o;
+          if (j < see.x || j >= see.y || !((there >> o) & 1)) s[kt][i] = -INFINITY;
+        }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kt][i]);
+    top = fmaxf(top, other_half(top)) * c1;
+    // The maximum that weights refer to moves only when it is exceeded by 2^8: no weight passes 2^8,
+    // and the sums keep their 32 bits.
+    if (__any(top > m + 8.0f)) {
+      const float to = top > m + 8.0f ? top : m;
+      const float shrink = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+      m = to;
+      l *= shrink;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[d][i] *= shrink;
+    }
+    const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[kt][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][i], c1, -ref));
+        l += s[kt][i];
+      }
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f32x8 pv;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pv[i] = s[kt][8 * h + i];
+        // one rounding of each weight to the element type, which the matrix unit takes
+        const u32x4 p = narrow<E>(pv);
+        const int r = kw + kt * 32 + 16 * h + 4 * hf + ((lane & 15) >> 2);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const int col = d * 32 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4, cc = col >> 3;
+          const int at = (r * VPR + (cc ^ v_swz(r))) * 16 + (col & 7) * 2;
+          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KVX_LDS s16x4*)(sv + at));
+          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KVX_LDS s16x4*)(sv + at + 8 * VPR * 16));
+          const s16x8 va = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+          acc[d] = mfma(E(), __builtin_bit_cast(u32x4, va), p, acc[d]);
+        }
+      }
+    if (skipped) {
+      for (uint64_t todo = skipped; todo; todo &= todo - 1) {
+        const int o = __builtin_ctzll(todo), j = k0 + kw + o;
+        float pj = 0;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (kt * 32 + 8 * (i / 4) + 4 * hf + i % 4 == o) pj = s[kt][i];
+        pj += other_half(pj);
+        // one product of the weights and the row of V, whose sums only the rows that see it take
+        const int b = block_of(div, j);
+        const char* p = (const char*)a.cache.base + table[b] * a.cache.block_stride_bytes +
+                        (int64_t)(j - b * div.size) * a.cache.token_stride_bytes + a.cache.kv_stride_bytes +
+                        g * a.cache.head_stride_bytes;
+        const u32x4 pb = narrow<E>(f32x8{hf == 0 ? pj : 0.0f, 0, 0, 0, 0, 0, 0, 0});
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const int e = d * 32 + n;
+          u32x4 va = {0, 0, 0, 0};
+          if (hf == 0 && e < a.cache.head_dim) va[0] = gload<uint16_t>(p + e * 2);
+          const f32x16 with = mfma(E(), va, pb, acc[d]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[d][i] = j < see.x || j >= see.y ? acc[d][i] : with[i];
+        }
+      }
+    }
+    if constexpr (KEYS) __builtin_amdgcn_wave_barrier();
+    else lds_barrier();
+  }
+  if (errs) raise(a.err, errs);
+  l += other_half(l);
+
+  if constexpr (KEYS) {
+    // join the wavefronts: weights of each one's sum, then the sums themselves through LDS
+    float* const sm = (float*)smem;
+    __syncthreads();
+    if (lane < 32) {
+      sm[w * 32 + n] = m;
+      sm[128 + w * 32 + n] = l;
+    }
+    __syncthreads();
+    float top = -INFINITY, total = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, sm[i * 32 + n]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) total += sm[128 + i * 32 + n] * __builtin_amdgcn_exp2f(sm[i * 32 + n] - ref);
+    const float mine = __builtin_amdgcn_exp2f(m - ref);
+    __syncthreads();
+    // [wavefront][row][16-byte pieces, swizzled by row]
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = acc[d][4 * i + e] * mine;
+        const int piece = d * 8 + 2 * i + hf;
+        *(f32x4*)(smem + ((w * 32 + n) * (DP / 4) + (piece ^ (n & 15))) * 16) = v;
+      }
+    m = top;
+    l = total;
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      // wavefront w takes register quad w of each 32 dimensions
+      f32x4 v = {};
+      const int piece = d * 8 + 2 * w + hf;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v += *(const f32x4*)(smem + ((i * 32 + n) * (DP / 4) + (piece ^ (n & 15))) * 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[d][e] = v[e];
+    }
+  }
+
+  if (!used) return;
+  const float inv = l == 0 ? 0.0f : 1.0f / l;
+  const int64_t flat = q_row * a.num_heads + head;
+  constexpr int QUADS = KEYS ? 1 : 4;  // register quads of each 32 dimensions that this lane stores
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < QUADS; ++i) {
+      const int e = d * 32 + 8 * (KEYS ? w : i) + 4 * hf;
+      if (e >= a.cache.head_dim) continue;
+      f32x4 v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = l == 0 ? 0.0f : acc[d][4 * i + k] * inv;
+      if (sp.count > 1) {
+        gstore(sp.acc + (split * sp.rows + flat) * a.cache.head_dim + e, v);
+      } else {
+        gstore((char*)a.out.base + q_row * a.out.token_stride + head * a.out.head_stride + e * 2,
+               __builtin_convertvector(v, typename E::V4));
+      }
+    }
+  if (hf == 0 && (!KEYS || w == 0)) {
+    const float lse2 = l == 0 ? -INFINITY : m + __builtin_amdgcn_logf(l);
+    if (sp.count > 1) sp.lse[split * sp.rows + flat] = lse2;
+    else if (a.lse) a.lse[flat] = lse2 * kLn2;
+  }
+}
+
+// Joins the parts of split contexts: out = sum_s 2^(lse_s - top) o_s / sum_s 2^(lse_s - top). A thread takes
+// four dimensions of one row; parts that saw nothing are not read.
+template <class E>
+__global__ __launch_bounds__(256) void join_kernel(AttendArgs a, Split sp) {
+  const int quads = a.cache.head_dim / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, flat = i / quads;
+  if (flat >= sp.rows) return;
+  const int64_t t = flat / a.num_heads;
+  if (t < a.batch.q_offsets[0] || t >= a.batch.q_offsets[a.batch.num_reqs]) return;
+  const int e = (int)(i - flat * quads) * 4;
+  float top = -INFINITY;
+  for (int s = 0; s < sp.count; ++s) top = fmaxf(top, sp.lse[s * sp.rows + flat]);
+  const float ref = top == -INFINITY ? 0.0f : top;
+  float total = 0;
+  f32x4 o = {};
+  for (int s = 0; s < sp.count; ++s) {
+    const float lse = sp.lse[s * sp.rows + flat];
+    if (lse == -INFINITY) continue;
+    const float wgt = __builtin_amdgcn_exp2f(lse - ref);
+    total += wgt;
+    o += wgt * gload<f32x4>(sp.acc + (s * sp.rows + flat) * a.cache.head_dim + e);
+  }
+  const float inv = total == 0 ? 0.0f : 1.0f / total;
+  gstore((char*)a.out.base + t * a.out.token_stride + (flat - t * a.num_heads) * a.out.head_stride + e * 2,
+         __builtin_convertvector(o * inv, typename E::V4));
+  if (e == 0 && a.lse) a.lse[flat] = total == 0 ? -INFINITY : (ref + __builtin_amdgcn_logf(total)) * kLn2;
+}
+
+// The launch shape of a batch: by slots (KEYS) where a request's rows of one KV head fit one tile of
+// 32, and as many parts of the contexts as fill the GPU with two workgroups a CU, each at least
+// kMinPart slots long.
+constexpr int kMinPart = 512, kMaxParts = 64, kFill = 512;
+
+struct Plan {
+  bool keys;
+  int32_t tiles, parts;
+};
+Plan plan_attention(const kvx_paged_cache& c, const kvx_batch& b, int32_t num_heads) {
+  const int64_t group = num_heads / c.num_kv_heads;
+  const int64_t longest = b.max_query_len < b.num_tokens ? b.max_query_len : b.num_tokens;
+  Plan p;
+  p.keys = longest * group <= 32;
+  const int64_t rows = p.keys ? 32 : 128;
+  p.tiles = (int32_t)(b.num_tokens * group / rows + b.num_reqs);
+  int64_t busy = b.num_reqs * ((longest * group + rows - 1) / rows);
+  if (busy > p.tiles) busy = p.tiles;
+  busy = (busy > 0 ? busy : 1) * c.num_kv_heads;
+  int64_t parts = kFill / busy;
+  if (parts > b.max_context_len / kMinPart) parts = b.max_context_len / kMinPart;
+  if (parts > kMaxParts) parts = kMaxParts;
+  p.parts = parts > 1 ? (int32_t)parts : 1;
+  return p;
+}
+
+int64_t part_bytes(const kvx_paged_cache& c, const kvx_batch& b, int32_t num_heads) {
+  return b.num_tokens * num_heads * 4 * ((int64_t)c.head_dim + 4);
+}
+
+template <class E, int DP>
+void launch_attend(const AttendArgs& a, BlockDiv div, const Split& sp, bool keys, hipStream_t stream) {
+  const dim3 grid((unsigned)sp.tiles, a.cache.num_kv_heads, sp.count);
+  if (keys) attend_kernel<E, DP, true><<<grid, 256, 0, stream>>>(a, div, sp);
+  else attend_kernel<E, DP, false><<<grid, 256, 0, stream>>>(a, div, sp);
+}
+
+template <class E>
+void launch_attend_dims(const AttendArgs& a, BlockDiv div, const Split& sp, bool keys, hipStream_t stream) {
+  if (a.cache.head_dim <= 64) launch_attend<E, 64>(a, div, sp, keys, stream);
+  else if (a.cache.head_dim <= 128) launch_attend<E, 128>(a, div, sp, keys, stream);
+  else launch_attend<E, 256>(a, div, sp, keys, stream);
+  if (sp.count > 1) {
+    const int64_t threads = sp.rows * (a.cache.head_dim / 4);
+    join_kernel<E><<<dim3((unsigned)((threads + 255) / 256)), 256, 0, stream>>>(a, sp);
+  }
 }
 
 // One wavefront a slot of one KV head, a query row at a time.
@@ -102,11 +538,11 @@ __global__ __launch_bounds__(64) void mass_simple(MassArgs m, BlockDiv div) {
   const AttendArgs& a = m.at;
   const int r = blockIdx.z, g = blockIdx.y, lane = threadIdx.x;
   int32_t errs = 0;
-  int64_t c = context_of(a, r, &errs);
-  if (c > m.mass_width) {
-    c = m.mass_width;
-    errs |= KVX_DEVERR_TABLE_RANGE;
-  }
+  const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size, len = a.batch.context_lens[r];
+  const int64_t full = clamp64(len, 0, cap);
+  int64_t c = full;
+  if (c > m.mass_width) c = m.mass_width;
+  if (c != len) errs |= KVX_DEVERR_TABLE_RANGE;
   const int64_t b0 = a.batch.q_offsets[r], e0 = a.batch.q_offsets[r + 1];
   const int64_t b = b0 < 0 ? 0 : b0, e = e0 > a.batch.num_tokens ? a.batch.num_tokens : e0;
   if (b != b0 || e != e0 || e < b) errs |= KVX_DEVERR_OFFSETS;
@@ -125,7 +561,6 @@ __global__ __launch_bounds__(64) void mass_simple(MassArgs m, BlockDiv div) {
     float total = 0;
     bool any = false;
     for (int64_t t = b; t < e; ++t) {
-      const int64_t full = context_of(a, r, &errs);
       const int64_t last = a.causal ? full - (e - t) : full - 1;
       if (j > last || j <= last - a.window) continue;
       any = true;
@@ -151,14 +586,24 @@ __global__ __launch_bounds__(64) void mass_simple(MassArgs m, BlockDiv div) {
 }  // namespace
 
 hipError_t launch_attention(const AttendArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.batch.num_tokens * a.num_heads));
+  const Plan p = plan_attention(a.cache, a.batch, a.num_heads);
+  Split sp = {p.parts, p.tiles, a.cache.num_kv_heads, nullptr, nullptr, a.batch.num_tokens * a.num_heads};
+  const int64_t fit = a.workspace_bytes / part_bytes(a.cache, a.batch, a.num_heads);
+  if (sp.count > fit) sp.count = fit > 1 ? (int32_t)fit : 1;
+  if (sp.count > 1) {
+    sp.acc = (float*)a.workspace;  // first: rows of 16-byte vectors
+    sp.lse = sp.acc + sp.count * sp.rows * a.cache.head_dim;
+  }
   const BlockDiv div = block_div(a.cache.block_size);
-  if (a.cache.dtype == KVX_DTYPE_BF16) attend_simple<Bf16><<<grid, 64, 0, stream>>>(a, div);
-  else attend_simple<Fp16><<<grid, 64, 0, stream>>>(a, div);
+  if (a.cache.dtype == KVX_DTYPE_BF16) launch_attend_dims<Bf16>(a, div, sp, p.keys, stream);
+  else launch_attend_dims<Fp16>(a, div, sp, p.keys, stream);
   return hipGetLastError();
 }
 
-int64_t attention_workspace(const kvx_paged_cache&, const kvx_batch&, int32_t) { return 0; }
+int64_t attention_workspace(const kvx_paged_cache& c, const kvx_batch& b, int32_t num_heads) {
+  const Plan p = plan_attention(c, b, num_heads);
+  return p.parts > 1 ? p.parts * part_bytes(c, b, num_heads) : 0;
+}
 
 hipError_t launch_mass(const MassArgs& m, hipStream_t stream) {
   const kvx_batch& b = m.at.batch;

@@ -35,9 +35,9 @@ kvx_status check_cache(const kvx_paged_cache* c) {
   return KVX_SUCCESS;
 }
 
-// A block table's shape; slots of a request stay below 2^31.
+// A block table's shape; slots of a request, and those of a few tiles behind them, stay below 2^31.
 bool table_ok(int64_t reqs, int64_t cols, int64_t row, int32_t block_size) {
-  return cols >= 0 && row >= cols && extent_ok(reqs, row) && cols <= kInt32Max / block_size;
+  return cols >= 0 && row >= cols && extent_ok(reqs, row) && cols <= (kInt32Max - 65536) / block_size;
 }
 
 kvx_status check_rows(int64_t tokens, int64_t heads, int64_t token_stride, int64_t head_stride) {

@@ -130,8 +130,8 @@ kvx_status kvx_rope_and_cache(const kvx_paged_cache* cache, const void* query,
  * negative one, or a table entry outside the cache raises KVX_DEVERR_TABLE_RANGE or
  * KVX_DEVERR_BLOCK_RANGE and the slots concerned count as not seen; offsets that decrease or leave
  * [0, num_tokens] raise KVX_DEVERR_OFFSETS and are clamped.
- * Errors: INVALID_ARGUMENT (num_tokens*num_heads or max_blocks_per_req*block_size of 2^31 or more
- * among them), MISALIGNED.
+ * Errors: INVALID_ARGUMENT (num_tokens*num_heads of 2^31 or more and max_blocks_per_req*block_size
+ * above 2^31 - 65537 among them), MISALIGNED.
  */
 kvx_status kvx_paged_attention(const kvx_paged_cache* cache, const kvx_batch* batch,
                                const void* query, int64_t query_token_stride_bytes,
