@@ -120,6 +120,13 @@ __device__ __forceinline__ bool non_finite(u32x4 v) {
   return bad;
 }
 
+// The same value, computed where it stands: keeps what the rare branches of a loop need out of the
+// registers of the loop.
+__device__ __forceinline__ int here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // Barrier for data passed through LDS: global loads stay in flight across it.
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -146,17 +153,19 @@ struct Split {
 //   KEYS = false: the four wavefronts hold 32 rows each and share every 64 slots staged in LDS.
 //   KEYS = true (up to 32 rows): they hold the same rows and 32 slots each of every 128, meet
 //     only at the end, and need no barrier before it: bound by the bytes of K and V.
-// K and V go from memory to registers one tile ahead and then to LDS, 16-byte pieces XOR-swizzled by
-// slot so that the reads of 16 rows (K), or of 4 slots x 64 bytes (V), fall on different banks.
+// K and V go from memory to registers one tile ahead and then to LDS, in rows padded so that the reads of
+// 16 rows (K: 16 bytes a row), or of 4 slots x 64 bytes (V: 64 bytes a row), fall on different banks;
+// padding, unlike a swizzle, leaves every address one register and a constant.
 template <class E, int DP, bool KEYS>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendArgs a, BlockDiv div, Split sp) {
   constexpr int ROWS = KEYS ? 32 : 128, BN = KEYS ? 128 : 64, KW = BN / 4;
   constexpr int VPR = DP / 8, RPI = 64 / VPR, NI = KW / RPI;
   constexpr int KT = KEYS ? 1 : 2, KSTEPS = DP / 16, DT = DP / 32;
-  __shared__ __align__(16) char smem[2 * BN * DP * 2 + BN];
+  constexpr int KROW = DP * 2 + 16, VROW = DP * 2 + 64;  // bytes of a row in LDS
+  __shared__ __align__(16) char smem[BN * (KROW + VROW) + BN];
   char* const sk = smem;
-  char* const sv = smem + BN * DP * 2;
-  uint8_t* const flags = (uint8_t*)(smem + 2 * BN * DP * 2);
+  char* const sv = smem + BN * KROW;
+  uint8_t* const flags = (uint8_t*)(smem + BN * (KROW + VROW));
 
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, hf = lane >> 5;
@@ -200,14 +209,16 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   const char* const kbase = (const char*)a.cache.base + g * a.cache.head_stride_bytes + (c < vecs ? c : 0) * 16;
   const int32_t* const table = a.batch.block_table + x.r * a.batch.bt_row_stride;
   const int cols = (int)a.batch.max_blocks_per_req;
-  auto k_swz = [](int r) { return VPR == 8 ? (r >> 1) & 7 : r & 15; };
-  auto v_swz = [](int r) { return VPR == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; };
+  char* const sk_put = sk + (w * KW + sub) * KROW + c * 16;
+  char* const sv_put = sv + (w * KW + sub) * VROW + c * 16;
+  const int kw = KEYS ? w * KW : 0;  // first slot of a tile that this wavefront computes
+  const char* const sk_get = sk + (kw + n) * KROW + hf * 16;
+  const char* const sv_get = sv + (kw + 4 * hf + ((lane & 15) >> 2)) * VROW + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
   if (vecs < VPR && c >= vecs) {  // the padding of every row is zero, once
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int r = w * KW + i * RPI + sub;
-      *(u32x4*)(sk + (r * VPR + (c ^ k_swz(r))) * 16) = u32x4{0, 0, 0, 0};
-      *(u32x4*)(sv + (r * VPR + (c ^ v_swz(r))) * 16) = u32x4{0, 0, 0, 0};
+      *(u32x4*)(sk_put + i * RPI * KROW) = u32x4{0, 0, 0, 0};
+      *(u32x4*)(sv_put + i * RPI * VROW) = u32x4{0, 0, 0, 0};
     }
   }
 
@@ -253,28 +264,30 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
     const bool inner = k0 >= last.x && k0 + BN <= first.y;
     if (lane < KW) flags[w * KW + lane] = (ok_mask >> lane) & 1;
     if (~ok_mask) {
+      const uint32_t mine = (uint32_t)(ok_mask >> here(sub));
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        if (!((ok_mask >> (i * RPI + sub)) & 1)) rk[i] = rv[i] = u32x4{0, 0, 0, 0};
+        if (!(mine & (1u << (i * RPI)))) rk[i] = rv[i] = u32x4{0, 0, 0, 0};
     }
     if (!inner) {
       // A weight of zero times a NaN or infinity is NaN: rows of V that hold one are left out of the
       // products and added below for the query rows that see them.
+      const int from = here(sub);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const uint64_t bad = __ballot(c < vecs && non_finite<E>(rv[i]));
-        if (VPR == 64 ? bad : (bad >> (sub * VPR)) & ((1ull << (VPR & 63)) - 1)) {
+        if (bad == 0) continue;
+        if ((bad >> (from * VPR)) & ((1ull << VPR) - 1)) {
           rv[i] = u32x4{0, 0, 0, 0};
-          if (c == 0) flags[w * KW + i * RPI + sub] = 3;
+          if (c == 0) flags[w * KW + i * RPI + from] = 3;
         }
       }
     }
     if (c < vecs) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int r = w * KW + i * RPI + sub;
-        *(u32x4*)(sk + (r * VPR + (c ^ k_swz(r))) * 16) = rk[i];
-        *(u32x4*)(sv + (r * VPR + (c ^ v_swz(r))) * 16) = rv[i];
+        *(u32x4*)(sk_put + i * RPI * KROW) = rk[i];
+        *(u32x4*)(sv_put + i * RPI * VROW) = rv[i];
       }
     }
     if constexpr (KEYS) __builtin_amdgcn_wave_barrier();
@@ -284,7 +297,6 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
       id = load_id(t + 2);
     }
 
-    const int kw = KEYS ? w * KW : 0;  // first slot of the tile that this wavefront computes
     const uint8_t flag = flags[kw + (lane & (KT * 32 - 1))];
     // one bit a slot of this wavefront; with KEYS its 32 slots are read twice
     const uint64_t there = __ballot(flag & 1), skipped = __ballot((flag & 2) && lane < KT * 32);
@@ -292,19 +304,21 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
       s[kt] = f32x16{};
-      const int r = kw + kt * 32 + n;
 #pragma unroll
       for (int st = 0; st < KSTEPS; ++st)
-        s[kt] = mfma(E(), *(const u32x4*)(sk + (r * VPR + ((2 * st + hf) ^ k_swz(r))) * 16), q[st], s[kt]);
+        s[kt] = mfma(E(), *(const u32x4*)(sk_get + kt * 32 * KROW + st * 32), q[st], s[kt]);
     }
     if (!inner || ~there) {
+      const int at = here(k0 + kw + 4 * hf), lo = see.x - at, hi = see.y - at;
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
+      for (int kt = 0; kt < KT; ++kt) {
+        const uint32_t mine = (uint32_t)(there >> (kt * 32)) >> here(4 * hf);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int o = kt * 32 + 8 * (i / 4) + 4 * hf + i % 4, j = k0 + kw + o;
-          if (j < see.x || j >= see.y || !((there >> o) & 1)) s[kt][i] = -INFINITY;
+          const int o = 8 * (i / 4) + i % 4;
+          if (kt * 32 + o < lo || kt * 32 + o >= hi || !(mine & (1u << o))) s[kt][i] = -INFINITY;
         }
+      }
     }
     float top = -INFINITY;
 #pragma unroll
@@ -341,13 +355,11 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
         for (int i = 0; i < 8; ++i) pv[i] = s[kt][8 * h + i];
         // one rounding of each weight to the element type, which the matrix unit takes
         const u32x4 p = narrow<E>(pv);
-        const int r = kw + kt * 32 + 16 * h + 4 * hf + ((lane & 15) >> 2);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const int col = d * 32 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4, cc = col >> 3;
-          const int at = (r * VPR + (cc ^ v_swz(r))) * 16 + (col & 7) * 2;
-          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KVX_LDS s16x4*)(sv + at));
-          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KVX_LDS s16x4*)(sv + at + 8 * VPR * 16));
+          const char* at = sv_get + (kt * 32 + 16 * h) * VROW + d * 64;
+          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KVX_LDS s16x4*)at);
+          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KVX_LDS s16x4*)(at + 8 * VROW));
           const s16x8 va = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
           acc[d] = mfma(E(), __builtin_bit_cast(u32x4, va), p, acc[d]);
         }
@@ -360,22 +372,23 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (kt * 32 + 8 * (i / 4) + 4 * hf + i % 4 == o) pj = s[kt][i];
+            if (kt * 32 + 8 * (i / 4) + i % 4 == o - here(4 * hf)) pj = s[kt][i];
         pj += other_half(pj);
-        // one product of the weights and the row of V, whose sums only the rows that see it take
+        if (j < see.x || j >= see.y) continue;
         const int b = block_of(div, j);
         const char* p = (const char*)a.cache.base + table[b] * a.cache.block_stride_bytes +
                         (int64_t)(j - b * div.size) * a.cache.token_stride_bytes + a.cache.kv_stride_bytes +
-                        g * a.cache.head_stride_bytes;
-        const u32x4 pb = narrow<E>(f32x8{hf == 0 ? pj : 0.0f, 0, 0, 0, 0, 0, 0, 0});
+                        g * a.cache.head_stride_bytes + hf * 8;
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const int e = d * 32 + n;
-          u32x4 va = {0, 0, 0, 0};
-          if (hf == 0 && e < a.cache.head_dim) va[0] = gload<uint16_t>(p + e * 2);
-          const f32x16 with = mfma(E(), va, pb, acc[d]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[d][i] = j < see.x || j >= see.y ? acc[d][i] : with[i];
+          for (int i = 0; i < 4; ++i) {
+            if (d * 32 + 8 * i >= a.cache.head_dim) break;
+            const f32x4 v = __builtin_convertvector(gload<typename E::V4>(p + d * 64 + i * 16), f32x4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[d][4 * i + e] += pj * v[e];
+          }
+          __builtin_amdgcn_sched_barrier(0);  // a few at a time: this branch must not set the registers of the loop
         }
       }
     }
