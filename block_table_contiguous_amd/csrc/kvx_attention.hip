@@ -545,55 +545,130 @@ void launch_attend_dims(const AttendArgs& a, BlockDiv div, const Split& sp, bool
   }
 }
 
-// One wavefront a slot of one KV head, a query row at a time.
-template <class E>
-__global__ __launch_bounds__(64) void mass_simple(MassArgs m, BlockDiv div) {
-  const AttendArgs& a = m.at;
-  const int r = blockIdx.z, g = blockIdx.y, lane = threadIdx.x;
-  int32_t errs = 0;
-  const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size, len = a.batch.context_lens[r];
-  const int64_t full = clamp64(len, 0, cap);
-  int64_t c = full;
-  if (c > m.mass_width) c = m.mass_width;
-  if (c != len) errs |= KVX_DEVERR_TABLE_RANGE;
-  const int64_t b0 = a.batch.q_offsets[r], e0 = a.batch.q_offsets[r + 1];
-  const int64_t b = b0 < 0 ? 0 : b0, e = e0 > a.batch.num_tokens ? a.batch.num_tokens : e0;
-  if (b != b0 || e != e0 || e < b) errs |= KVX_DEVERR_OFFSETS;
+// --------------------------------------------------------------------------------------
+// attention mass
+// --------------------------------------------------------------------------------------
+
+// A wavefront owns 64 slots of one KV head: their K stays in registers, the query rows pass by 32 at a time, and the
+// weights exp(x - lse) of S^T = K Q^T add up in the score registers' own layout, a partial sum a
+// lane; the lanes' sums meet once at the end, through LDS. Every slot belongs to one wavefront, so
+// nothing is joined between workgroups and the order of the sum is fixed. For a few rows the
+// bytes of K bound it, for many the exponentials and products.
+constexpr int kMassSlots = 256;  // of a workgroup
+
+template <class E, int DP>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void mass_kernel(MassArgs ma, BlockDiv div) {
+  constexpr int KSTEPS = DP / 16, LROW = 36;  // floats of a slot's partial sums in LDS
+  __shared__ __align__(16) float part[4][64 * LROW];
+  const AttendArgs& a = ma.at;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 31, hf = lane >> 5, g = blockIdx.y, r = blockIdx.z;
   const int group = a.num_heads / a.cache.num_kv_heads, vecs = a.cache.head_dim / 8;
-  for (int64_t j = blockIdx.x; j < c; j += gridDim.x) {
-    const int blk = block_of(div, (int32_t)j);
-    const int64_t id = a.batch.block_table[r * a.batch.bt_row_stride + blk];
-    if (id < 0 || id >= a.cache.num_blocks) {
-      errs |= KVX_DEVERR_BLOCK_RANGE;
-      continue;
-    }
-    const char* row = (const char*)a.cache.base + id * a.cache.block_stride_bytes +
-                      (int64_t)(j - (int64_t)blk * div.size) * a.cache.token_stride_bytes + g * a.cache.head_stride_bytes;
-    f32x8 kk = {};
-    if (lane < vecs) kk = widen<E>(gload<u32x4>(row + lane * 16));
-    float total = 0;
-    bool any = false;
-    for (int64_t t = b; t < e; ++t) {
-      const int64_t last = a.causal ? full - (e - t) : full - 1;
-      if (j > last || j <= last - a.window) continue;
-      any = true;
-      for (int i = 0; i < group; ++i) {
-        const int h = g * group + i;
-        const float lse = a.lse[t * a.num_heads + h];
-        if (lse == -INFINITY) continue;
-        float s = 0;
-        if (lane < vecs) {
-          const f32x8 q =
-              widen<E>(gload<u32x4>(a.query.base + t * a.query.token_stride + h * a.query.head_stride + lane * 16));
-          for (int x = 0; x < 8; ++x) s += q[x] * kk[x];
-        }
-        for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-        total += exp2f((s * a.scale - lse) * kLog2e);
+  const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size;
+  if (blockIdx.x == 0 && g == 0 && r == 0) check_batch(a, cap, tid, 256);
+  Rows x;
+  x.r = r;
+  x.q0 = clamp64(a.batch.q_offsets[r], 0, a.batch.num_tokens);
+  x.tokens = (int32_t)(clamp64(a.batch.q_offsets[r + 1], x.q0, a.batch.num_tokens) - x.q0);
+  x.context = a.cache.num_blocks > 0 ? (int32_t)clamp64(a.batch.context_lens[r], 0, cap) : 0;
+  int errs = 0;
+  if (x.context > ma.mass_width && blockIdx.x == 0) raise(a.err, KVX_DEVERR_TABLE_RANGE);
+  if (x.tokens == 0) return;
+  const int rows = x.tokens * group;
+  const int2 first = sees(a, x, 0), last = sees(a, x, x.tokens - 1);
+  const int end = last.y < ma.mass_width ? last.y : (int)ma.mass_width;
+  const float c1 = a.scale * kLog2e;
+  const int32_t* const table = a.batch.block_table + r * a.batch.bt_row_stride;
+
+  for (int64_t at = (int64_t)blockIdx.x * kMassSlots + w * 64; at < end; at += (int64_t)gridDim.x * kMassSlots) {
+    const int k0 = (int)at;
+    // K of slot k0 + 32 kt + n in registers; lanes look up one slot each
+    const int j = k0 + lane;
+    const bool in = j >= first.x && j < end;
+    const int32_t id = in ? table[block_of(div, j)] : -1;
+    const bool ok = in && (uint32_t)id < (uint64_t)a.cache.num_blocks;
+    if (in && !ok) errs |= KVX_DEVERR_BLOCK_RANGE;
+    const int64_t off = ok ? id * a.cache.block_stride_bytes +
+                                 (int64_t)(j - block_of(div, j) * div.size) * a.cache.token_stride_bytes
+                           : 0;
+    float* const mass = ma.mass + r * ma.mass_req_stride + g * ma.mass_head_stride + j;
+    float before = 0;
+    if (ok) before = gload<float>(mass);
+    u32x4 k[2][KSTEPS];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      const char* p = (const char*)a.cache.base + g * a.cache.head_stride_bytes + __shfl(off, kt * 32 + n);
+#pragma unroll
+      for (int st = 0; st < KSTEPS; ++st) {
+        const int c = 2 * st + hf;
+        k[kt][st] = gload<u32x4>(p + (c < vecs ? c : 0) * 16);
+        if (DP / 8 != vecs && c >= vecs) k[kt][st] = u32x4{0, 0, 0, 0};
       }
     }
-    if (any && lane == 0) m.mass[r * m.mass_req_stride + g * m.mass_head_stride + j] += total;
+    // the rows that see some of these slots
+    int row_from = 0, row_to = rows;
+    if (a.causal) {
+      const int64_t t0 = (int64_t)k0 - x.context + x.tokens, t1 = t0 + 64 + a.window;
+      if (t0 > 0) row_from = t0 < x.tokens ? (int)t0 * group : rows;
+      if (t1 < x.tokens) row_to = t1 > 0 ? (int)t1 * group : 0;
+    }
+    f32x16 sum[2] = {f32x16{}, f32x16{}};
+    for (int row0 = row_from; row0 < row_to; row0 += 32) {
+      const int row = row0 + n;
+      const bool used = row < row_to;
+      const int token = used ? row / group : 0, head = g * group + (used ? row - token * group : 0);
+      const char* p = a.query.base + (x.q0 + token) * a.query.token_stride + head * a.query.head_stride;
+      const float lse = used ? gload<float>(a.lse + (x.q0 + token) * a.num_heads + head) : -INFINITY;
+      u32x4 q[KSTEPS];
+#pragma unroll
+      for (int st = 0; st < KSTEPS; ++st) {
+        const int c = 2 * st + hf;
+        q[st] = gload<u32x4>(p + (c < vecs ? c : 0) * 16);
+        if (DP / 8 != vecs && c >= vecs) q[st] = u32x4{0, 0, 0, 0};
+      }
+      int2 see = sees(a, x, token);
+      if (lse == -INFINITY) see = {0, 0};
+      const bool whole = __all(see.x <= k0 && see.y >= k0 + 64);
+      const float ref = lse * kLog2e;
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        f32x16 s = {};
+#pragma unroll
+        for (int st = 0; st < KSTEPS; ++st) s = mfma(E(), k[kt][st], q[st], s);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c1, -ref));
+        if (!whole) {
+          const int at = here(k0 + kt * 32 + 4 * hf), lo = see.x - at, hi = see.y - at;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int o = 8 * (i / 4) + i % 4;
+            if (o < lo || o >= hi) s[i] = 0;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[kt][i] += s[i];
+      }
+    }
+    float* const mine = part[w];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mine[(kt * 32 + 8 * (i / 4) + 4 * hf + i % 4) * LROW + n] = sum[kt][i];
+    __builtin_amdgcn_wave_barrier();
+    f32x4 t = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += *(const f32x4*)(mine + lane * LROW + i * 4);
+    if (ok) gstore(mass, before + ((t[0] + t[1]) + (t[2] + t[3])));
+    __builtin_amdgcn_wave_barrier();
   }
-  if (errs && lane == 0) raise(a.err, errs);
+  if (errs) raise(a.err, errs);
+}
+
+template <class E>
+void launch_mass_dims(const MassArgs& m, BlockDiv div, dim3 grid, hipStream_t stream) {
+  if (m.at.cache.head_dim <= 64) mass_kernel<E, 64><<<grid, 256, 0, stream>>>(m, div);
+  else if (m.at.cache.head_dim <= 128) mass_kernel<E, 128><<<grid, 256, 0, stream>>>(m, div);
+  else mass_kernel<E, 256><<<grid, 256, 0, stream>>>(m, div);
 }
 
 }  // namespace
@@ -620,11 +695,14 @@ int64_t attention_workspace(const kvx_paged_cache& c, const kvx_batch& b, int32_
 
 hipError_t launch_mass(const MassArgs& m, hipStream_t stream) {
   const kvx_batch& b = m.at.batch;
-  const int64_t cap = b.max_blocks_per_req * m.at.cache.block_size;
-  const dim3 grid((unsigned)(cap < m.mass_width ? cap : m.mass_width), m.at.cache.num_kv_heads, b.num_reqs);
+  int64_t slots = b.max_blocks_per_req * m.at.cache.block_size;
+  if (slots > m.mass_width) slots = m.mass_width;
+  // as many workgroups as the hint asks for; they go on over the slots of a longer request
+  if (slots > b.max_context_len) slots = b.max_context_len > 0 ? b.max_context_len : 1;
+  const dim3 grid((unsigned)((slots + kMassSlots - 1) / kMassSlots), m.at.cache.num_kv_heads, b.num_reqs);
   const BlockDiv div = block_div(m.at.cache.block_size);
-  if (m.at.cache.dtype == KVX_DTYPE_BF16) mass_simple<Bf16><<<grid, 64, 0, stream>>>(m, div);
-  else mass_simple<Fp16><<<grid, 64, 0, stream>>>(m, div);
+  if (m.at.cache.dtype == KVX_DTYPE_BF16) launch_mass_dims<Bf16>(m, div, grid, stream);
+  else launch_mass_dims<Fp16>(m, div, grid, stream);
   return hipGetLastError();
 }
 

@@ -230,6 +230,7 @@ kvx_status kvx_evict_compact(const kvx_paged_cache* cache, const int32_t* block_
   const kvx_status st = check_cache(cache);
   if (st == KVX_ERR_INVALID_ARGUMENT) return st;
   if (num_reqs < 0 || num_heads < 1 || cache->num_kv_heads % num_heads != 0 || budget < 1 || budget > kInt32Max ||
+      cache->num_blocks == 0 || max_blocks_per_req < 1 || dst_max_blocks_per_req < 1 ||
       !table_ok(num_reqs, max_blocks_per_req, bt_row_stride, cache->block_size) ||
       !table_ok(num_reqs, dst_max_blocks_per_req, dst_bt_row_stride, cache->block_size) ||
       (int64_t)num_reqs * (2 * cache->num_kv_heads + num_heads) > kInt32Max || (mass == nullptr) != (mass_out == nullptr))
@@ -245,7 +246,7 @@ kvx_status kvx_evict_compact(const kvx_paged_cache* cache, const int32_t* block_
     return KVX_ERR_INVALID_ARGUMENT;
   if (st != KVX_SUCCESS) return st;
   if (num_reqs == 0) return KVX_SUCCESS;
-  if (!block_table || !dst_block_table || !keep || (cache->num_blocks > 0 && !cache->base))
+  if (!block_table || !dst_block_table || !keep || !cache->base)
     return KVX_ERR_INVALID_ARGUMENT;
   // one table in place: its rows are read the same way on both sides
   if (block_table == dst_block_table &&

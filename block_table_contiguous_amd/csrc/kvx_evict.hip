@@ -112,6 +112,12 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(SelectArgs a) {
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 8;
 
+// Every load of the workgroup has its value before any wavefront goes on to store.
+__device__ __forceinline__ void loads_landed() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+}
+
 // A workgroup moves one column: the K or V rows of one KV head of one request, or one row of
 // masses, a tile of slots at a time: all its loads, then all its stores. An ascending list has
 // keep[i] >= i, so a slot is read in its own tile or an earlier one; with the tiles of a column in
@@ -141,8 +147,7 @@ __global__ __launch_bounds__(kMoveThreads) void compact_kernel(CompactArgs a, Bl
         else if (k >= a.mass_width) errs |= KVX_DEVERR_TABLE_RANGE;
         else if (k >= 0) v[u] = in[k];
       }
-      __builtin_amdgcn_s_waitcnt(0);  // the loads have landed in every wave before any store
-      __syncthreads();
+      loads_landed();
 #pragma unroll
       for (int u = 0; u < kMoveUnroll; ++u) {
         const int64_t i = t0 + u * kMoveThreads + tid;
@@ -158,43 +163,55 @@ __global__ __launch_bounds__(kMoveThreads) void compact_kernel(CompactArgs a, Bl
     const int32_t* to = a.dst_table + r * a.dst_row;
     const uint32_t vecs = cache.head_dim / 8;
     const int tile_rows = kMoveThreads * kMoveUnroll / vecs;
+    // this thread's rows and pieces of a tile, the same in every tile
+    int row[kMoveUnroll], piece[kMoveUnroll];
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const uint32_t x = u * kMoveThreads + tid;
+      row[u] = x / vecs;
+      piece[u] = (x - row[u] * vecs) * 16;
+    }
     for (int64_t t0 = (int64_t)blockIdx.y * tile_rows; t0 < a.budget; t0 += (int64_t)gridDim.y * tile_rows) {
-      u32x4 v[kMoveUnroll];
-      char* dst[kMoveUnroll];
+      // Three rounds of loads, each issued whole: list entries, table entries, rows. What is not to be
+      // moved reads the first entry or row instead, and is not stored.
+      int32_t k[kMoveUnroll], sb[kMoveUnroll], db[kMoveUnroll];
+      bool move[kMoveUnroll];
 #pragma unroll
       for (int u = 0; u < kMoveUnroll; ++u) {
-        const uint32_t x = u * kMoveThreads + tid, row = x / vecs, c = x - row * vecs;
-        const int64_t i = t0 + row;
-        dst[u] = nullptr;
-        if ((int)row >= tile_rows || i >= a.budget) continue;
-        const int32_t k = keep[i];
-        if (k < 0) continue;
-        if (k < i) {
-          errs |= KVX_DEVERR_OFFSETS;
-          continue;
-        }
-        const int32_t sb = block_of(div, k), db = block_of(div, (int32_t)i);
-        if (sb >= a.src_cols || db >= a.dst_cols) {
-          errs |= KVX_DEVERR_TABLE_RANGE;
-          continue;
-        }
-        const int64_t s = from[sb], d = to[db];
-        if (s < 0 || s >= cache.num_blocks || d < 0 || d >= cache.num_blocks) {
-          errs |= KVX_DEVERR_BLOCK_RANGE;
-          continue;
-        }
-        if (in_place && k == i) continue;
-        const char* src = (const char*)cache.base + s * cache.block_stride_bytes +
-                          (int64_t)(k - sb * div.size) * cache.token_stride_bytes + at + c * 16;
-        dst[u] = (char*)cache.base + d * cache.block_stride_bytes +
-                 (int64_t)((int32_t)i - db * div.size) * cache.token_stride_bytes + at + c * 16;
+        move[u] = row[u] < tile_rows && t0 + row[u] < a.budget;
+        k[u] = gload<int32_t>(keep + (move[u] ? t0 + row[u] : 0));
+      }
+#pragma unroll
+      for (int u = 0; u < kMoveUnroll; ++u) {
+        const int32_t i = (int32_t)(t0 + row[u]);
+        move[u] = move[u] && k[u] >= 0;
+        if (move[u] && k[u] < i) errs |= KVX_DEVERR_OFFSETS, move[u] = false;
+        const int32_t s = block_of(div, k[u]), d = block_of(div, i);
+        if (move[u] && (s >= a.src_cols || d >= a.dst_cols)) errs |= KVX_DEVERR_TABLE_RANGE, move[u] = false;
+        k[u] = move[u] ? k[u] - s * div.size : 0;  // places in the blocks from here on
+        piece[u] = (piece[u] & 0xffff) | (move[u] && in_place && s == d && k[u] == i - d * div.size ? 1 << 16 : 0);
+        sb[u] = gload<int32_t>(from + (move[u] ? s : 0));
+        db[u] = gload<int32_t>(to + (move[u] ? d : 0));
+      }
+      u32x4 v[kMoveUnroll];
+#pragma unroll
+      for (int u = 0; u < kMoveUnroll; ++u) {
+        if (move[u] && ((uint32_t)sb[u] >= (uint64_t)cache.num_blocks || (uint32_t)db[u] >= (uint64_t)cache.num_blocks))
+          errs |= KVX_DEVERR_BLOCK_RANGE, move[u] = false;
+        move[u] = move[u] && !(piece[u] >> 16);
+        const char* src = (const char*)cache.base + at + (piece[u] & 0xffff);
+        if (move[u]) src += sb[u] * cache.block_stride_bytes + (int64_t)k[u] * cache.token_stride_bytes;
         v[u] = gload<u32x4>(src);
       }
-      __builtin_amdgcn_s_waitcnt(0);  // the loads have landed in every wave before any store
-      __syncthreads();
+      loads_landed();
 #pragma unroll
-      for (int u = 0; u < kMoveUnroll; ++u)
-        if (dst[u]) gstore(dst[u], v[u]);
+      for (int u = 0; u < kMoveUnroll; ++u) {
+        const int32_t i = (int32_t)(t0 + row[u]);
+        if (move[u])
+          gstore((char*)cache.base + db[u] * cache.block_stride_bytes +
+                     (int64_t)(i - block_of(div, i) * div.size) * cache.token_stride_bytes + at + (piece[u] & 0xffff),
+                 v[u]);
+      }
     }
   }
   if (errs) raise(a.err, errs);

@@ -204,7 +204,7 @@ kvx_status kvx_evict_select(const float* mass, int64_t mass_req_stride, int64_t 
  * Destination slots past the kept ones keep their bytes. An entry outside the tables' (or the
  * masses') width, or in a block id outside the cache, is skipped and raises KVX_DEVERR_TABLE_RANGE
  * or KVX_DEVERR_BLOCK_RANGE; one below its own index (no ascending list has it) is skipped and
- * raises KVX_DEVERR_OFFSETS.
+ * raises KVX_DEVERR_OFFSETS. The cache has at least one block, both tables at least one column.
  */
 kvx_status kvx_evict_compact(const kvx_paged_cache* cache, const int32_t* block_table,
                              int64_t max_blocks_per_req, int64_t bt_row_stride,

@@ -164,7 +164,8 @@ def test_compact_refusals():
     for kw in (dict(R=-1), dict(H=0), dict(H=3), dict(budget=0), dict(cols=9), dict(drow=7), dict(src=None), dict(dst=None),
                dict(keep=None), dict(m=P), dict(mo=P), dict(m=P, mo=2 * P, w=-1), dict(m=P, mo=2 * P, wo=-1),
                dict(m=P, mo=P),  # onto itself, but not in place
-               dict(dst=P, m=P, mo=P, mos=400), dict(dst=P, dcols=7), dict(c=cache(base=None))):
+               dict(dst=P, m=P, mo=P, mos=400), dict(dst=P, dcols=7), dict(c=cache(base=None)),
+               dict(c=cache(num_blocks=0)), dict(cols=0), dict(dcols=0)):
         assert compact(**kw) == INVALID, kw
     assert compact(c=cache(base=P + 8)) == MISALIGNED
     assert compact(R=0, src=None) == OK
