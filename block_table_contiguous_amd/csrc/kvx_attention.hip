@@ -171,9 +171,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   const int n = lane & 31, hf = lane >> 5;
   const int group = a.num_heads / a.cache.num_kv_heads, vecs = a.cache.head_dim / 8;
   const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size;
-  const int g = blockIdx.y, split = blockIdx.z;
-  if (blockIdx.x == 0 && g == 0 && split == 0) check_batch(a, cap, tid, 256);
-  const Rows x = find_rows<ROWS>(a, sp.tiles - 1 - blockIdx.x, group, cap, lane);
+  const int g = blockIdx.x % a.cache.num_kv_heads, split = blockIdx.y;
+  if (blockIdx.x == 0 && split == 0) check_batch(a, cap, tid, 256);
+  const Rows x = find_rows<ROWS>(a, sp.tiles - 1 - blockIdx.x / a.cache.num_kv_heads, group, cap, lane);
   const int row0 = x.tile * ROWS, rows = x.tokens * group;
   if (row0 >= rows) return;
 
@@ -529,7 +529,7 @@ int64_t part_bytes(const kvx_paged_cache& c, const kvx_batch& b, int32_t num_hea
 
 template <class E, int DP>
 void launch_attend(const AttendArgs& a, BlockDiv div, const Split& sp, bool keys, hipStream_t stream) {
-  const dim3 grid((unsigned)sp.tiles, a.cache.num_kv_heads, sp.count);
+  const dim3 grid((unsigned)(sp.tiles * a.cache.num_kv_heads), sp.count);
   if (keys) attend_kernel<E, DP, true><<<grid, 256, 0, stream>>>(a, div, sp);
   else attend_kernel<E, DP, false><<<grid, 256, 0, stream>>>(a, div, sp);
 }
@@ -549,42 +549,86 @@ void launch_attend_dims(const AttendArgs& a, BlockDiv div, const Split& sp, bool
 // attention mass
 // --------------------------------------------------------------------------------------
 
-// A wavefront owns 64 slots of one KV head: their K stays in registers, the query rows pass by 32 at a time, and the
-// weights exp(x - lse) of S^T = K Q^T add up in the score registers' own layout, a partial sum a
-// lane; the lanes' sums meet once at the end, through LDS. Every slot belongs to one wavefront, so
-// nothing is joined between workgroups and the order of the sum is fixed. For a few rows the
-// bytes of K bound it, for many the exponentials and products.
-constexpr int kMassSlots = 256;  // of a workgroup
-
-template <class E, int DP>
-__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void mass_kernel(MassArgs ma, BlockDiv div) {
-  constexpr int KSTEPS = DP / 16, LROW = 36;  // floats of a slot's partial sums in LDS
-  __shared__ __align__(16) float part[4][64 * LROW];
-  const AttendArgs& a = ma.at;
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n = lane & 31, hf = lane >> 5, g = blockIdx.y, r = blockIdx.z;
-  const int group = a.num_heads / a.cache.num_kv_heads, vecs = a.cache.head_dim / 8;
-  const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size;
-  if (blockIdx.x == 0 && g == 0 && r == 0) check_batch(a, cap, tid, 256);
+// The rows of a request that a mass kernel works on, and what it may touch of the masses.
+struct MassRows {
   Rows x;
+  int rows, from, end;  // query rows; slots [from, end) that some row sees and the masses hold
+};
+__device__ __forceinline__ bool mass_rows(const MassArgs& ma, int r, int group, int64_t cap, MassRows* m) {
+  const AttendArgs& a = ma.at;
+  Rows& x = m->x;
   x.r = r;
   x.q0 = clamp64(a.batch.q_offsets[r], 0, a.batch.num_tokens);
   x.tokens = (int32_t)(clamp64(a.batch.q_offsets[r + 1], x.q0, a.batch.num_tokens) - x.q0);
   x.context = a.cache.num_blocks > 0 ? (int32_t)clamp64(a.batch.context_lens[r], 0, cap) : 0;
-  int errs = 0;
-  if (x.context > ma.mass_width && blockIdx.x == 0) raise(a.err, KVX_DEVERR_TABLE_RANGE);
-  if (x.tokens == 0) return;
-  const int rows = x.tokens * group;
-  const int2 first = sees(a, x, 0), last = sees(a, x, x.tokens - 1);
-  const int end = last.y < ma.mass_width ? last.y : (int)ma.mass_width;
+  if (x.context > ma.mass_width && blockIdx.y == 0) raise(a.err, KVX_DEVERR_TABLE_RANGE);
+  if (x.tokens == 0) return false;
+  m->rows = x.tokens * group;
+  m->from = sees(a, x, 0).x;
+  const int last = sees(a, x, x.tokens - 1).y;
+  m->end = last < ma.mass_width ? last : (int)ma.mass_width;
+  return true;
+}
+
+// Loads a tile of rows as the memory holds them, 16 consecutive bytes a lane and whole rows by
+// neighbouring lanes, and passes it through LDS to the lanes that the products want it in: read
+// by those lanes directly, each would touch a line of its own, and the address unit, not
+// memory, would set the pace (a decode batch's masses: 108 us against 60).
+template <int DP, int TILE>
+struct RowTile {
+  static constexpr int VPR = DP / 8, RPI = 64 / VPR, NI = TILE / RPI, ROW = DP * 2 + 16;
+  u32x4 v[NI];
+  // where(i): address of row i * RPI + lane / VPR, whose piece lane % VPR this lane loads
+  template <class F>
+  __device__ __forceinline__ void load(F where, int lane, int vecs) {
+    const int c = lane % VPR, from = c < vecs ? c * 16 : 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) v[i] = gload<u32x4>(where(i) + from);
+  }
+  __device__ __forceinline__ void put(char* lds, int lane, int vecs) const {
+    const int c = lane % VPR;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      *(u32x4*)(lds + (i * RPI + lane / VPR) * ROW + c * 16) = VPR == vecs || c < vecs ? v[i] : u32x4{0, 0, 0, 0};
+  }
+};
+
+// A wavefront owns 64 slots of one KV head: their K stays in registers, the query rows pass by 32 at a
+// time (through LDS, for all four wavefronts), and the weights exp(x - lse) of S^T = K Q^T add up in the
+// score registers' own layout, a partial sum a lane; the lanes' sums meet once at the end, through
+// LDS. Every slot belongs to one wavefront, so nothing is joined between workgroups and the order of
+// the sum is fixed. The exponentials bound it, then the products.
+constexpr int kMassSlots = 256;  // of a workgroup
+constexpr int kMassFill = 4096;  // workgroups that fill the GPU with few rows
+
+template <class E, int DP>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void mass_kernel(MassArgs ma, BlockDiv div) {
+  typedef RowTile<DP, 32> KTile;
+  typedef RowTile<DP, 8> QTile;  // a wavefront's share of 32 rows
+  constexpr int KSTEPS = DP / 16, LROW = 36, ROW = KTile::ROW;  // LROW: floats of a slot's partial sums in LDS
+  constexpr int OWN = 32 * ROW > 64 * LROW * 4 ? 32 * ROW : 64 * LROW * 4;
+  __shared__ __align__(16) char smem[4 * OWN + 2 * 32 * ROW];
+  const AttendArgs& a = ma.at;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 31, hf = lane >> 5, g = blockIdx.x, r = blockIdx.z;
+  const int group = a.num_heads / a.cache.num_kv_heads, vecs = a.cache.head_dim / 8;
+  const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size;
+  if (blockIdx.y == 0 && g == 0 && r == 0) check_batch(a, cap, tid, 256);
+  MassRows m;
+  if (!mass_rows(ma, r, group, cap, &m)) return;
+  const Rows& x = m.x;
   const float c1 = a.scale * kLog2e;
   const int32_t* const table = a.batch.block_table + r * a.batch.bt_row_stride;
+  char* const own = smem + w * OWN;       // K on its way to registers, then partial sums
+  char* const qs = smem + 4 * OWN;        // two tiles of query rows
+  int errs = 0;
 
-  for (int64_t at = (int64_t)blockIdx.x * kMassSlots + w * 64; at < end; at += (int64_t)gridDim.x * kMassSlots) {
-    const int k0 = (int)at;
-    // K of slot k0 + 32 kt + n in registers; lanes look up one slot each
+  for (int64_t at = (int64_t)blockIdx.y * kMassSlots; at < m.end; at += (int64_t)gridDim.y * kMassSlots) {
+    if (at + kMassSlots <= m.from) continue;
+    const int k0 = (int)at + w * 64;
+    // lanes look up one slot each
     const int j = k0 + lane;
-    const bool in = j >= first.x && j < end;
+    const bool in = j >= m.from && j < m.end;
     const int32_t id = in ? table[block_of(div, j)] : -1;
     const bool ok = in && (uint32_t)id < (uint64_t)a.cache.num_blocks;
     if (in && !ok) errs |= KVX_DEVERR_BLOCK_RANGE;
@@ -595,61 +639,83 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void mass_kernel(MassArgs m
     float before = 0;
     if (ok) before = gload<float>(mass);
     u32x4 k[2][KSTEPS];
+    {
+      KTile t[2];
+      const char* const base = (const char*)a.cache.base + g * a.cache.head_stride_bytes;
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-      const char* p = (const char*)a.cache.base + g * a.cache.head_stride_bytes + __shfl(off, kt * 32 + n);
+      for (int kt = 0; kt < 2; ++kt)
+        t[kt].load([&](int i) { return base + __shfl(off, kt * 32 + i * KTile::RPI + lane / KTile::VPR); }, lane, vecs);
 #pragma unroll
-      for (int st = 0; st < KSTEPS; ++st) {
-        const int c = 2 * st + hf;
-        k[kt][st] = gload<u32x4>(p + (c < vecs ? c : 0) * 16);
-        if (DP / 8 != vecs && c >= vecs) k[kt][st] = u32x4{0, 0, 0, 0};
+      for (int kt = 0; kt < 2; ++kt) {
+        t[kt].put(own, lane, vecs);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int st = 0; st < KSTEPS; ++st) k[kt][st] = *(const u32x4*)(own + n * ROW + st * 32 + hf * 16);
+        __builtin_amdgcn_wave_barrier();
       }
     }
-    // the rows that see some of these slots
-    int row_from = 0, row_to = rows;
+    // the rows that see some of the workgroup's slots
+    int row_from = 0, row_to = m.rows;
     if (a.causal) {
-      const int64_t t0 = (int64_t)k0 - x.context + x.tokens, t1 = t0 + 64 + a.window;
-      if (t0 > 0) row_from = t0 < x.tokens ? (int)t0 * group : rows;
+      const int64_t t0 = at - x.context + x.tokens, t1 = t0 + kMassSlots + a.window;
+      if (t0 > 0) row_from = t0 < x.tokens ? (int)t0 * group : m.rows;
       if (t1 < x.tokens) row_to = t1 > 0 ? (int)t1 * group : 0;
     }
     f32x16 sum[2] = {f32x16{}, f32x16{}};
-    for (int row0 = row_from; row0 < row_to; row0 += 32) {
-      const int row = row0 + n;
-      const bool used = row < row_to;
-      const int token = used ? row / group : 0, head = g * group + (used ? row - token * group : 0);
-      const char* p = a.query.base + (x.q0 + token) * a.query.token_stride + head * a.query.head_stride;
-      const float lse = used ? gload<float>(a.lse + (x.q0 + token) * a.num_heads + head) : -INFINITY;
-      u32x4 q[KSTEPS];
+    QTile q;
+    int2 see;
+    float lse;
+    auto row_of = [&](int row, int* token, int* head) {  // a row past the last reads the first token's
+      *token = row < row_to ? row / group : 0;
+      *head = g * group + (row < row_to ? row - *token * group : 0);
+    };
+    auto load_rows = [&](int row0) {
+      q.load([&](int i) {
+        int token, head;
+        row_of(row0 + w * 8 + i * QTile::RPI + lane / QTile::VPR, &token, &head);
+        return a.query.base + (x.q0 + token) * a.query.token_stride + head * a.query.head_stride;
+      }, lane, vecs);
+      int token, head;
+      row_of(row0 + n, &token, &head);
+      lse = gload<float>(a.lse + (x.q0 + token) * a.num_heads + head);
+      see = row0 + n < row_to ? sees(a, x, token) : int2{0, 0};
+    };
+    if (row_from < row_to) load_rows(row_from);
+    int turn = 0;
+    for (int row0 = row_from; row0 < row_to; row0 += 32, turn ^= 1) {
+      char* const tile = qs + turn * 32 * ROW;
+      q.put(tile + w * 8 * ROW, lane, vecs);
+      const float ref = lse * kLog2e;
+      const int2 now = lse == -INFINITY ? int2{0, 0} : see;
+      // The other tile is written next, which every wavefront has read before this barrier.
+      lds_barrier();
+      if (row0 + 32 < row_to) load_rows(row0 + 32);
+      if (!__any(now.y > k0 && now.x < k0 + 64)) continue;
+      f32x16 s[2] = {f32x16{}, f32x16{}};
 #pragma unroll
       for (int st = 0; st < KSTEPS; ++st) {
-        const int c = 2 * st + hf;
-        q[st] = gload<u32x4>(p + (c < vecs ? c : 0) * 16);
-        if (DP / 8 != vecs && c >= vecs) q[st] = u32x4{0, 0, 0, 0};
+        const u32x4 qf = *(const u32x4*)(tile + n * ROW + st * 32 + hf * 16);
+        s[0] = mfma(E(), k[0][st], qf, s[0]);
+        s[1] = mfma(E(), k[1][st], qf, s[1]);
       }
-      int2 see = sees(a, x, token);
-      if (lse == -INFINITY) see = {0, 0};
-      const bool whole = __all(see.x <= k0 && see.y >= k0 + 64);
-      const float ref = lse * kLog2e;
+      const bool whole = __all(now.x <= k0 && now.y >= k0 + 64);
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
-        f32x16 s = {};
 #pragma unroll
-        for (int st = 0; st < KSTEPS; ++st) s = mfma(E(), k[kt][st], q[st], s);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c1, -ref));
+        for (int i = 0; i < 16; ++i) s[kt][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][i], c1, -ref));
         if (!whole) {
-          const int at = here(k0 + kt * 32 + 4 * hf), lo = see.x - at, hi = see.y - at;
+          const int to = here(k0 + kt * 32 + 4 * hf), lo = now.x - to, hi = now.y - to;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int o = 8 * (i / 4) + i % 4;
-            if (o < lo || o >= hi) s[i] = 0;
+            if (o < lo || o >= hi) s[kt][i] = 0;
           }
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum[kt][i] += s[i];
+        for (int i = 0; i < 16; ++i) sum[kt][i] += s[kt][i];
       }
     }
-    float* const mine = part[w];
+    float* const mine = (float*)own;
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
@@ -659,16 +725,139 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void mass_kernel(MassArgs m
 #pragma unroll
     for (int i = 0; i < 8; ++i) t += *(const f32x4*)(mine + lane * LROW + i * 4);
     if (ok) gstore(mass, before + ((t[0] + t[1]) + (t[2] + t[3])));
-    __builtin_amdgcn_wave_barrier();
+    lds_barrier();  // the query tiles and the partial sums are free again
+  }
+  if (errs) raise(a.err, errs);
+}
+
+// The same for up to 32 query rows of a KV head, a decode step's: the rows stay in registers and the
+// slots pass by, 32 a wavefront and step with the next step's K on its way: the bytes of K bound it.
+template <class E, int DP>
+__global__ __launch_bounds__(256, DP <= 128 ? 3 : 2) void mass_few_kernel(MassArgs ma, BlockDiv div, int span) {
+  typedef RowTile<DP, 32> Tile;
+  constexpr int KSTEPS = DP / 16, LROW = 36, ROW = Tile::ROW;
+  constexpr int OWN = 32 * ROW > 32 * LROW * 4 ? 32 * ROW : 32 * LROW * 4;
+  __shared__ __align__(16) char smem[4 * OWN];
+  const AttendArgs& a = ma.at;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 31, hf = lane >> 5, g = blockIdx.x, r = blockIdx.z;
+  const int group = a.num_heads / a.cache.num_kv_heads, vecs = a.cache.head_dim / 8;
+  const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size;
+  if (blockIdx.y == 0 && g == 0 && r == 0) check_batch(a, cap, tid, 256);
+  MassRows m;
+  if (!mass_rows(ma, r, group, cap, &m)) return;
+  const Rows& x = m.x;
+  const int32_t* const table = a.batch.block_table + r * a.batch.bt_row_stride;
+  const char* const base = (const char*)a.cache.base + g * a.cache.head_stride_bytes;
+  float* const masses = ma.mass + r * ma.mass_req_stride + g * ma.mass_head_stride;
+  const float c1 = a.scale * kLog2e;
+  char* const own = smem + w * OWN;  // K, then the weights
+  int errs = 0;
+
+  u32x4 q[KSTEPS];
+  int2 see;
+  float ref;
+  auto load_rows = [&](int row0) {
+    const int row = row0 + n;
+    const bool used = row < m.rows;
+    const int token = used ? row / group : 0, head = g * group + (used ? row - token * group : 0);
+    const char* p = a.query.base + (x.q0 + token) * a.query.token_stride + head * a.query.head_stride;
+    const float lse = gload<float>(a.lse + (x.q0 + token) * a.num_heads + head);
+#pragma unroll
+    for (int st = 0; st < KSTEPS; ++st) {
+      const int c = 2 * st + hf;
+      q[st] = gload<u32x4>(p + (c < vecs ? c : 0) * 16);
+      if (DP / 8 != vecs && c >= vecs) q[st] = u32x4{0, 0, 0, 0};
+    }
+    see = used && lse != -INFINITY ? sees(a, x, token) : int2{0, 0};
+    ref = lse * kLog2e;
+  };
+
+  for (int64_t at = (int64_t)blockIdx.y * span; at < m.end; at += (int64_t)gridDim.y * span) {
+    // this wavefront's steps: slots from, from + 128, ... below to
+    const int to = at + span < m.end ? (int)at + span : m.end;
+    const int skip = m.from > at ? (int)((m.from - at) / 128 * 128) : 0;
+    const int from = (int)at + skip + w * 32;
+    if (from >= to) continue;
+    bool ok;
+    Tile k;
+    float before;
+    auto look_up = [&](int k0) -> int32_t {  // lanes l and l + 32: slot k0 + l
+      const int j = k0 + n;
+      return j >= m.from && j < to ? table[block_of(div, j)] : -1;
+    };
+    auto load_k = [&](int k0, int32_t id) {
+      const int j = k0 + n;
+      const bool in = j >= m.from && j < to;
+      ok = in && (uint32_t)id < (uint64_t)a.cache.num_blocks;
+      if (in && !ok) errs |= KVX_DEVERR_BLOCK_RANGE;
+      const int64_t off = ok ? id * a.cache.block_stride_bytes +
+                                   (int64_t)(j - block_of(div, j) * div.size) * a.cache.token_stride_bytes
+                             : 0;
+      k.load([&](int i) { return base + __shfl(off, i * Tile::RPI + lane / Tile::VPR); }, lane, vecs);
+      before = ok ? gload<float>(masses + j) : 0.0f;
+    };
+    // one pass over the slots; more only where a request has more rows than the hint said
+    for (int row0 = 0; row0 < m.rows; row0 += 32) {
+      load_k(from, look_up(from));
+      int32_t id = from + 128 < to ? look_up(from + 128) : -1;
+      load_rows(row0);
+      for (int k0 = from; k0 < to; k0 += 128) {
+        const bool store = ok;
+        const float old = before;
+        k.put(own, lane, vecs);
+        __builtin_amdgcn_wave_barrier();
+        if (k0 + 128 < to) {
+          load_k(k0 + 128, id);
+          id = k0 + 256 < to ? look_up(k0 + 256) : -1;
+        }
+        f32x16 s = {};
+#pragma unroll
+        for (int st = 0; st < KSTEPS; ++st)
+          s = mfma(E(), *(const u32x4*)(own + n * ROW + st * 32 + hf * 16), q[st], s);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c1, -ref));
+        if (!__all(see.x <= k0 && see.y >= k0 + 32)) {
+          const int origin = here(k0 + 4 * hf), lo = see.x - origin, hi = see.y - origin;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int o = 8 * (i / 4) + i % 4;
+            if (o < lo || o >= hi) s[i] = 0;
+          }
+        }
+        float* const mine = (float*)own;
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mine[(8 * (i / 4) + 4 * hf + i % 4) * LROW + n] = s[i];
+        __builtin_amdgcn_wave_barrier();
+        // lane l sums half of slot l % 32's weights
+        float total = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 t = *(const f32x4*)(mine + n * LROW + hf * 16 + i * 4);
+          total += (t[0] + t[1]) + (t[2] + t[3]);
+        }
+        total += other_half(total);
+        __builtin_amdgcn_wave_barrier();
+        if (store && hf == 0) gstore(masses + k0 + n, old + total);
+      }
+    }
   }
   if (errs) raise(a.err, errs);
 }
 
 template <class E>
-void launch_mass_dims(const MassArgs& m, BlockDiv div, dim3 grid, hipStream_t stream) {
-  if (m.at.cache.head_dim <= 64) mass_kernel<E, 64><<<grid, 256, 0, stream>>>(m, div);
-  else if (m.at.cache.head_dim <= 128) mass_kernel<E, 128><<<grid, 256, 0, stream>>>(m, div);
-  else mass_kernel<E, 256><<<grid, 256, 0, stream>>>(m, div);
+void launch_mass_dims(const MassArgs& m, BlockDiv div, dim3 grid, int span, hipStream_t stream) {
+  const int dim = m.at.cache.head_dim;
+  if (span) {
+    if (dim <= 64) mass_few_kernel<E, 64><<<grid, 256, 0, stream>>>(m, div, span);
+    else if (dim <= 128) mass_few_kernel<E, 128><<<grid, 256, 0, stream>>>(m, div, span);
+    else mass_few_kernel<E, 256><<<grid, 256, 0, stream>>>(m, div, span);
+  } else {
+    if (dim <= 64) mass_kernel<E, 64><<<grid, 256, 0, stream>>>(m, div);
+    else if (dim <= 128) mass_kernel<E, 128><<<grid, 256, 0, stream>>>(m, div);
+    else mass_kernel<E, 256><<<grid, 256, 0, stream>>>(m, div);
+  }
 }
 
 }  // namespace
@@ -699,10 +888,22 @@ hipError_t launch_mass(const MassArgs& m, hipStream_t stream) {
   if (slots > m.mass_width) slots = m.mass_width;
   // as many workgroups as the hint asks for; they go on over the slots of a longer request
   if (slots > b.max_context_len) slots = b.max_context_len > 0 ? b.max_context_len : 1;
-  const dim3 grid((unsigned)((slots + kMassSlots - 1) / kMassSlots), m.at.cache.num_kv_heads, b.num_reqs);
+  const int64_t longest = b.max_query_len < b.num_tokens ? b.max_query_len : b.num_tokens;
+  const int64_t lists = (int64_t)b.num_reqs * m.at.cache.num_kv_heads;
+  int64_t per = kMassSlots;
+  int span = 0;
+  if (longest * (m.at.num_heads / m.at.cache.num_kv_heads) <= 32) {
+    // slots of a workgroup: a whole number of steps of its four wavefronts, few enough to fill the GPU
+    per = (slots * lists / kMassFill + 127) / 128 * 128;
+    if (per < 128) per = 128;
+    if (per > 4096) per = 4096;
+    span = (int)per;
+  }
+  const int64_t pieces = (slots + per - 1) / per;
+  const dim3 grid(m.at.cache.num_kv_heads, (unsigned)(pieces < 65535 ? pieces : 65535), b.num_reqs);
   const BlockDiv div = block_div(m.at.cache.block_size);
-  if (m.at.cache.dtype == KVX_DTYPE_BF16) launch_mass_dims<Bf16>(m, div, grid, stream);
-  else launch_mass_dims<Fp16>(m, div, grid, stream);
+  if (m.at.cache.dtype == KVX_DTYPE_BF16) launch_mass_dims<Bf16>(m, div, grid, span, stream);
+  else launch_mass_dims<Fp16>(m, div, grid, span, stream);
   return hipGetLastError();
 }
 

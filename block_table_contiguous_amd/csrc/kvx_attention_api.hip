@@ -53,7 +53,7 @@ kvx_status check_batch(const kvx_paged_cache* c, const kvx_batch* b, int32_t num
   if (!b || b->num_reqs < 0 || b->num_reqs > 65535 || b->num_tokens < 0 || b->max_query_len < 0 ||
       b->max_context_len < 0 || num_heads < 1 || num_heads % c->num_kv_heads != 0 ||
       !table_ok(b->num_reqs, b->max_blocks_per_req, b->bt_row_stride, c->block_size) ||
-      b->num_tokens > kInt32Max / num_heads)
+      b->num_tokens > kInt32Max / num_heads || (int64_t)b->num_reqs * c->num_kv_heads > kInt32Max / 2)
     return KVX_ERR_INVALID_ARGUMENT;
   return st;
 }
