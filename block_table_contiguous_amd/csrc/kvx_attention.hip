@@ -470,31 +470,57 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
 }
 
 // Joins the parts of split contexts: out = sum_s 2^(lse_s - top) o_s / sum_s 2^(lse_s - top). A thread takes
-// four dimensions of one row; parts that saw nothing are not read.
-template <class E>
+// four dimensions of one row and every PG-th part, PG threads a row and dimension: with few rows the
+// parts are read side by side (64 parts of 32 rows: 65 -> 6 us). Parts that saw nothing are not read.
+template <class E, int PG>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, Split sp) {
-  const int quads = a.cache.head_dim / 4;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, flat = i / quads;
-  if (flat >= sp.rows) return;
+  __shared__ f32x4 sums[256];
+  __shared__ float tops[256], totals[256];
+  const int quads = a.cache.head_dim / 4, per = 256 / PG;
+  const int tid = threadIdx.x, pg = tid / per;
+  const int64_t i = (int64_t)blockIdx.x * per + tid % per, flat = i / quads;
   const int64_t t = flat / a.num_heads;
-  if (t < a.batch.q_offsets[0] || t >= a.batch.q_offsets[a.batch.num_reqs]) return;
+  const bool used = flat < sp.rows && t >= a.batch.q_offsets[0] && t < a.batch.q_offsets[a.batch.num_reqs];
   const int e = (int)(i - flat * quads) * 4;
-  float top = -INFINITY;
-  for (int s = 0; s < sp.count; ++s) top = fmaxf(top, sp.lse[s * sp.rows + flat]);
-  const float ref = top == -INFINITY ? 0.0f : top;
-  float total = 0;
+  float top = -INFINITY, total = 0;
   f32x4 o = {};
-  for (int s = 0; s < sp.count; ++s) {
-    const float lse = sp.lse[s * sp.rows + flat];
-    if (lse == -INFINITY) continue;
-    const float wgt = __builtin_amdgcn_exp2f(lse - ref);
-    total += wgt;
-    o += wgt * gload<f32x4>(sp.acc + (s * sp.rows + flat) * a.cache.head_dim + e);
+  if (used) {
+    for (int s = pg; s < sp.count; s += PG) top = fmaxf(top, sp.lse[s * sp.rows + flat]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll 4
+    for (int s = pg; s < sp.count; s += PG) {
+      const float lse = sp.lse[s * sp.rows + flat];
+      if (lse == -INFINITY) continue;
+      const float wgt = __builtin_amdgcn_exp2f(lse - ref);
+      total += wgt;
+      o += wgt * gload<f32x4>(sp.acc + (s * sp.rows + flat) * a.cache.head_dim + e);
+    }
   }
+  if constexpr (PG > 1) {
+    sums[tid] = o;
+    tops[tid] = top;
+    totals[tid] = total;
+    __syncthreads();
+    if (pg) return;
+#pragma unroll
+    for (int k = 1; k < PG; ++k) top = fmaxf(top, tops[k * per + tid]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    total = 0;
+    o = f32x4{};
+#pragma unroll
+    for (int k = 0; k < PG; ++k) {
+      const float m = tops[k * per + tid];
+      if (m == -INFINITY) continue;
+      const float wgt = __builtin_amdgcn_exp2f(m - ref);
+      total += wgt * totals[k * per + tid];
+      o += wgt * sums[k * per + tid];
+    }
+  }
+  if (!used) return;
   const float inv = total == 0 ? 0.0f : 1.0f / total;
   gstore((char*)a.out.base + t * a.out.token_stride + (flat - t * a.num_heads) * a.out.head_stride + e * 2,
          __builtin_convertvector(o * inv, typename E::V4));
-  if (e == 0 && a.lse) a.lse[flat] = total == 0 ? -INFINITY : (ref + __builtin_amdgcn_logf(total)) * kLn2;
+  if (e == 0 && a.lse) a.lse[flat] = total == 0 ? -INFINITY : (top + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
 // The launch shape of a batch: by slots (KEYS) where a request's rows of one KV head fit one tile of
@@ -541,7 +567,8 @@ void launch_attend_dims(const AttendArgs& a, BlockDiv div, const Split& sp, bool
   else launch_attend<E, 256>(a, div, sp, keys, stream);
   if (sp.count > 1) {
     const int64_t threads = sp.rows * (a.cache.head_dim / 4);
-    join_kernel<E><<<dim3((unsigned)((threads + 255) / 256)), 256, 0, stream>>>(a, sp);
+    if (sp.count <= 4) join_kernel<E, 1><<<dim3((unsigned)((threads + 255) / 256)), 256, 0, stream>>>(a, sp);
+    else join_kernel<E, 8><<<dim3((unsigned)((threads + 31) / 32)), 256, 0, stream>>>(a, sp);
   }
 }
 
