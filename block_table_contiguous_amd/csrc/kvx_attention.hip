@@ -31,6 +31,36 @@ __device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) {
   return x < lo ? lo : x > hi ? hi : x;
 }
 
+// Values that are the same in every lane, kept in scalar registers.
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  return (int64_t)(uint32_t)uniform((int32_t)x) | (int64_t)uniform((int32_t)(x >> 32)) << 32;
+}
+// One lane's value in all.
+__device__ __forceinline__ int32_t lane_of(int32_t x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
+__device__ __forceinline__ int64_t lane_of(int64_t x, int lane) {
+  return (int64_t)(uint32_t)lane_of((int32_t)x, lane) | (int64_t)lane_of((int32_t)(x >> 32), lane) << 32;
+}
+
+// Request r: its rows and slots, clamped to the tensors.
+__device__ __forceinline__ Rows request(const AttendArgs& a, int r, int64_t cap) {
+  Rows x;
+  x.r = r;
+  x.tile = 0;
+  x.q0 = clamp64(a.batch.q_offsets[r], 0, a.batch.num_tokens);
+  x.tokens = (int32_t)(clamp64(a.batch.q_offsets[r + 1], x.q0, a.batch.num_tokens) - x.q0);
+  x.context = a.cache.num_blocks > 0 ? (int32_t)clamp64(a.batch.context_lens[r], 0, cap) : 0;
+  return x;
+}
+// The same of a request that all lanes ask for.
+__device__ __forceinline__ Rows request_uniform(const AttendArgs& a, int r, int64_t cap) {
+  Rows x = request(a, uniform(r), cap);
+  x.q0 = uniform(x.q0);
+  x.tokens = uniform(x.tokens);
+  x.context = uniform(x.context);
+  return x;
+}
+
 // One workgroup of a launch looks every request's offsets and contexts over.
 __device__ void check_batch(const AttendArgs& a, int64_t cap, int tid, int threads) {
   int errs = 0;
@@ -42,48 +72,124 @@ __device__ void check_batch(const AttendArgs& a, int64_t cap, int tid, int threa
   if (errs) raise(a.err, errs);
 }
 
-// The request of a tile: a 64-way search over the offsets, one probe a lane and round (one round
-// up to 64 requests). All lanes get the same answer; whatever the offsets hold, r is a request.
-template <int ROWS>
-__device__ __forceinline__ Rows find_rows(const AttendArgs& a, int32_t tile, int group, int64_t cap, int lane) {
-  int lo = 0, len = a.batch.num_reqs;
-  int64_t begin, end, context;
-  for (;;) {
-    const int step = (len + 63) / 64;
-    const int i = lane * step < len ? lo + lane * step : lo;
-    begin = clamp64(a.batch.q_offsets[i], 0, a.batch.num_tokens);
-    end = a.batch.q_offsets[i + 1];
-    context = a.batch.context_lens[i];
-    const bool at = lane * step < len && begin * group / ROWS + i <= tile;
-    const int hit = __popcll(__ballot(at));
-    const int pick = hit ? hit - 1 : 0;
-    if (step == 1) {
-      begin = __shfl(begin, pick);
-      end = __shfl(end, pick);
-      context = __shfl(context, pick);
-      lo += pick;
-      break;
-    }
-    lo += pick * step;
-    len = len - pick * step < step ? len - pick * step : step;
-  }
-  Rows x;
-  x.r = __builtin_amdgcn_readfirstlane(lo);
-  x.q0 = begin;
-  x.tokens = (int32_t)(clamp64(end, begin, a.batch.num_tokens) - begin);
-  x.context = a.cache.num_blocks > 0 ? (int32_t)clamp64(context, 0, cap) : 0;
-  x.tile = tile - (int32_t)(begin * group / ROWS + lo);
-  x.tokens = __builtin_amdgcn_readfirstlane(x.tokens);
-  x.context = __builtin_amdgcn_readfirstlane(x.context);
-  x.tile = __builtin_amdgcn_readfirstlane(x.tile);
-  return x;
-}
-
 // The slots [lo, hi) that new token i of a request sees.
 __device__ __forceinline__ int2 sees(const AttendArgs& a, const Rows& x, int token) {
   const int64_t hi = a.causal ? (int64_t)x.context - x.tokens + token + 1 : (int64_t)x.context;
   const int64_t lo = hi - a.window;
   return {(int)(lo < 0 ? 0 : lo), (int)(hi < 0 ? 0 : hi)};
+}
+
+// The request of a tile: a 64-way search over the offsets, one probe a lane and round (one round
+// up to 64 requests). All lanes get the same answer; whatever the offsets hold, r is a request.
+template <int ROWS>
+__device__ __forceinline__ Rows find_rows(const AttendArgs& a, int32_t tile, int group, int64_t cap, int lane) {
+  int lo = 0, len = a.batch.num_reqs;
+  int64_t begin;
+  for (;;) {
+    const int step = (len + 63) / 64;
+    const int i = lane * step < len ? lo + lane * step : lo;
+    begin = clamp64(a.batch.q_offsets[i], 0, a.batch.num_tokens);
+    const bool at = lane * step < len && begin * group / ROWS + i <= tile;
+    const int hit = __popcll(__ballot(at));
+    const int pick = hit ? hit - 1 : 0;
+    lo += pick * step;
+    if (step == 1) break;
+    len = len - pick * step < step ? len - pick * step : step;
+  }
+  Rows x = request_uniform(a, lo, cap);
+  x.tile = tile - (int32_t)(x.q0 * group / ROWS + x.r);
+  return x;
+}
+
+// Shared work: the tiles of all requests in a row, each of its request's nominal number of steps (tiles
+// of slots that any of the request's rows sees, at least one), cut into equal shares for the
+// workgroups of one KV head. A share begins and ends anywhere, so a batch of any lengths is even; a tile
+// that several shares meet in is joined from its parts, which lie in consecutive slots of the
+// workspace: the part of share i in tile q is in slot i + q, since either number grows by
+// one from each part to the next.
+struct Shares {
+  int64_t steps;  // of all requests
+  int32_t count;  // shares that are not empty: the first `longer` have each + 1 steps, the others each
+  int32_t longer;
+  int64_t each;
+};
+// a / b of non-negative numbers; the 64-bit division costs an order of magnitude more than the 32-bit one
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+template <int ROWS, int BN>
+__device__ __forceinline__ void extent(const AttendArgs& a, const Rows& x, int group, int32_t* tiles, int32_t* steps) {
+  *tiles = (int32_t)(((int64_t)x.tokens * group + ROWS - 1) / ROWS);
+  const int lo = sees(a, x, 0).x, hi = sees(a, x, x.tokens - 1).y;
+  *steps = hi > lo ? (hi + BN - 1) / BN - lo / BN : 1;
+}
+// 64 requests of the batch, one a lane: their tiles and steps, and those of all requests before them.
+struct Requests {
+  Rows x;
+  int32_t tiles, steps, tile0;
+  int64_t step0;
+};
+template <int ROWS, int BN>
+__device__ __forceinline__ Requests sixty_four(const AttendArgs& a, int group, int64_t cap, int lane, int r0, int32_t tile0,
+                                               int64_t step0) {
+  Requests q = {};
+  if (r0 + lane < a.batch.num_reqs) {
+    q.x = request(a, r0 + lane, cap);
+    extent<ROWS, BN>(a, q.x, group, &q.tiles, &q.steps);
+  }
+  int64_t sum = (int64_t)q.tiles * q.steps;
+  int32_t num = q.tiles;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t s = __shfl_up(sum, d);
+    const int32_t t = __shfl_up(num, d);
+    if (lane >= d) sum += s, num += t;
+  }
+  q.tile0 = tile0 + num - q.tiles;
+  q.step0 = step0 + sum - (int64_t)q.tiles * q.steps;
+  return q;
+}
+// Counts the steps of the batch, and finds the request for which holds(shares, a lane's request) is
+// true: its lane's values in every lane, steps == 0 where there is none.
+template <int ROWS, int BN, class F>
+__device__ __forceinline__ Requests locate(const AttendArgs& a, int group, int64_t cap, int lane, int shares, Shares* all,
+                                           F holds) {
+  Requests q = {};
+  const int reqs = a.batch.num_reqs;
+  for (int r0 = 0; r0 < reqs; r0 += 64)
+    q = sixty_four<ROWS, BN>(a, group, cap, lane, r0, lane_of(q.tile0 + q.tiles, 63),
+                             lane_of(q.step0 + (int64_t)q.tiles * q.steps, 63));
+  all->steps = lane_of(q.step0 + (int64_t)q.tiles * q.steps, 63);
+  all->count = all->steps < shares ? (int32_t)all->steps : shares;
+  if (all->count == 0) return {};
+  all->each = quotient(all->steps, all->count);
+  all->longer = (int32_t)(all->steps - all->each * all->count);
+  Requests f = q;
+  for (int r0 = 0;; r0 += 64) {
+    if (reqs > 64)  // up to 64 requests the first pass holds them all
+      f = sixty_four<ROWS, BN>(a, group, cap, lane, r0, r0 ? lane_of(f.tile0 + f.tiles, 63) : 0,
+                               r0 ? lane_of(f.step0 + (int64_t)f.tiles * f.steps, 63) : 0);
+    const uint64_t there = __ballot(f.tiles > 0 && holds(*all, f));
+    if (there) {
+      const int l = __builtin_ctzll(there);
+      return {{r0 + l, lane_of(f.x.context, l), lane_of(f.x.tokens, l), 0, lane_of(f.x.q0, l)},
+              lane_of(f.tiles, l), lane_of(f.steps, l), lane_of(f.tile0, l), lane_of(f.step0, l)};
+    }
+    if (r0 + 64 >= reqs) return {};
+  }
+}
+__device__ __forceinline__ int64_t share_begin(const Shares& s, int i) {
+  return s.each * i + (i < s.longer ? i : s.longer);
+}
+__device__ __forceinline__ int share_of(const Shares& s, int64_t step) {  // the share that step falls into
+  const int64_t split = (s.each + 1) * s.longer;
+  return step < split ? (int)quotient(step, s.each + 1) : s.longer + (int)quotient(step - split, s.each);
+}
+
+__device__ __forceinline__ int2 sees_uniform(const AttendArgs& a, const Rows& x, int token) {
+  const int2 s = sees(a, x, uniform(token));
+  return {uniform(s.x), uniform(s.y)};
 }
 
 // --------------------------------------------------------------------------------------
@@ -120,6 +226,16 @@ __device__ __forceinline__ bool non_finite(u32x4 v) {
   return bad;
 }
 
+// A kernel's first argument, read from the argument segment where it stands: the loops' registers
+// need not hold what only their ends use.
+template <class T>
+__device__ __forceinline__ const T& argument() {
+  const __attribute__((address_space(4))) char* p =
+      (const __attribute__((address_space(4))) char*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const T*)p;
+}
+
 // The same value, computed where it stands: keeps what the rare branches of a loop need out of the
 // registers of the loop.
 __device__ __forceinline__ int here(int x) {
@@ -139,10 +255,10 @@ __device__ __forceinline__ void lds_barrier() {
 // --------------------------------------------------------------------------------------
 
 struct Split {
-  int32_t count, tiles, kv_heads;  // parts a context is cut into; row tiles
-  float* lse;                      // [count][rows], base 2; null where count == 1
-  float* acc;                      // [count][rows][head_dim]
-  int64_t rows;
+  int32_t shares;  // workgroups of a KV head that share the work evenly; 0: one a tile of rows
+  int32_t tiles;   // tiles of rows, at most
+  float* acc;      // [slot][KV head][row of the tile][head_dim], and the base-2 lse of each row
+  float* lse;
 };
 
 // One pass over the slots with a running maximum and sum. Scores are computed transposed, S^T = K Q^T, so that a lane
@@ -153,11 +269,13 @@ struct Split {
 //   KEYS = false: the four wavefronts hold 32 rows each and share every 64 slots staged in LDS.
 //   KEYS = true (up to 32 rows): they hold the same rows and 32 slots each of every 128, meet
 //     only at the end, and need no barrier before it: bound by the bytes of K and V.
+//   SHARED: the grid's workgroups take equal shares of the whole batch's steps (see Shares).
 // K and V go from memory to registers one tile ahead and then to LDS, in rows padded so that the reads of
 // 16 rows (K: 16 bytes a row), or of 4 slots x 64 bytes (V: 64 bytes a row), fall on different banks;
 // padding, unlike a swizzle, leaves every address one register and a constant.
-template <class E, int DP, bool KEYS>
-__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendArgs a, BlockDiv div, Split sp) {
+template <class E, int DP, bool KEYS, bool SHARED>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendArgs args, BlockDiv div, Split sp) {
+  const AttendArgs a = argument<AttendArgs>();
   constexpr int ROWS = KEYS ? 32 : 128, BN = KEYS ? 128 : 64, KW = BN / 4;
   constexpr int VPR = DP / 8, RPI = 64 / VPR, NI = KW / RPI;
   constexpr int KT = KEYS ? 1 : 2, KSTEPS = DP / 16, DT = DP / 32;
@@ -167,15 +285,59 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   char* const sv = smem + BN * KROW;
   uint8_t* const flags = (uint8_t*)(smem + BN * (KROW + VROW));
 
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform((int32_t)(tid >> 6));
   const int n = lane & 31, hf = lane >> 5;
   const int group = a.num_heads / a.cache.num_kv_heads, vecs = a.cache.head_dim / 8;
   const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size;
-  const int g = blockIdx.x % a.cache.num_kv_heads, split = blockIdx.y;
-  if (blockIdx.x == 0 && split == 0) check_batch(a, cap, tid, 256);
-  const Rows x = find_rows<ROWS>(a, sp.tiles - 1 - blockIdx.x / a.cache.num_kv_heads, group, cap, lane);
+  const int g = blockIdx.x % a.cache.num_kv_heads, index = blockIdx.x / a.cache.num_kv_heads;
+  if (blockIdx.x == 0) check_batch(a, cap, tid, 256);
+
+  // the padding of every row is zero, once
+  const int c = lane % VPR, sub = lane / VPR;  // the 16-byte piece and row this lane stages
+  char* const sk_put = sk + (w * KW + sub) * KROW + c * 16;
+  char* const sv_put = sv + (w * KW + sub) * VROW + c * 16;
+  const int kw = KEYS ? w * KW : 0;  // first slot of a tile that this wavefront computes
+  const char* const sk_get = sk + (kw + n) * KROW + hf * 16;
+  const char* const sv_get = sv + (kw + 4 * hf + ((lane & 15) >> 2)) * VROW + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+  auto clear_padding = [&]() {
+    if (vecs < VPR && c >= vecs) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        *(u32x4*)(sk_put + i * RPI * KROW) = u32x4{0, 0, 0, 0};
+        *(u32x4*)(sv_put + i * RPI * VROW) = u32x4{0, 0, 0, 0};
+      }
+    }
+  };
+  clear_padding();
+
+  // the tiles of rows, and the steps of each, that this workgroup computes
+  Rows x;
+  Shares all;
+  int32_t tiles = 0, steps = 1, tile0 = 0, from = 0, to = 1;  // steps [from, to) of tile x.tile
+  int64_t left = 1;                                           // steps of this share, with those
+  if constexpr (SHARED) {
+    const Requests q = locate<ROWS, BN>(a, group, cap, lane, sp.shares, &all, [&](const Shares& s, const Requests& q) {
+      const int64_t begin = share_begin(s, index);
+      return index < s.count && q.step0 <= begin && begin < q.step0 + (int64_t)q.tiles * q.steps;
+    });
+    if (q.steps == 0) return;
+    const int64_t begin = share_begin(all, index);
+    left = share_begin(all, index + 1) - begin;
+    tile0 = q.tile0;
+    tiles = q.tiles;
+    steps = q.steps;
+    x = q.x;
+    x.tile = (int32_t)quotient(begin - q.step0, steps);
+    from = (int32_t)(begin - q.step0 - (int64_t)x.tile * steps);
+  } else {
+    x = find_rows<ROWS>(a, sp.tiles - 1 - index, group, cap, lane);
+    if ((int64_t)x.tile * ROWS >= (int64_t)x.tokens * group) return;
+  }
+  int errs = 0;
+  for (;;) {
+  const AttendArgs a = argument<AttendArgs>();
+  if constexpr (SHARED) to = from + left < steps ? (int)(from + left) : steps;
   const int row0 = x.tile * ROWS, rows = x.tokens * group;
-  if (row0 >= rows) return;
 
   // this lane's row, what it sees, and what any row of the workgroup sees
   const int row = row0 + (KEYS ? 0 : w * 32) + n;
@@ -185,13 +347,19 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   int2 see = sees(a, x, token);
   if (!used) see = {0, 0};
   const int last_row = row0 + ROWS < rows ? row0 + ROWS - 1 : rows - 1;
-  const int2 first = sees(a, x, row0 / group), last = sees(a, x, last_row / group);
+  const int2 first = sees_uniform(a, x, row0 / group), last = sees_uniform(a, x, last_row / group);
   const int kend = last.y;
   const int t_first = first.x / BN, t_all = (kend + BN - 1) / BN - t_first;
   int tb = t_first, te = t_first + (t_all > 0 ? t_all : 0);
-  if (sp.count > 1) {
-    tb = t_first + (int)((int64_t)(te - t_first) * split / sp.count);
-    te = t_first + (int)((int64_t)(te - t_first) * (split + 1) / sp.count);
+  if constexpr (SHARED) {
+    if (t_all == steps) {
+      tb = t_first + from;
+      te = t_first + to;
+    } else {  // a tile whose rows see less than all of the request's: its steps in proportion
+      const int64_t mine = te - tb;
+      te = tb + (int)quotient(mine * to, steps);
+      tb = tb + (int)quotient(mine * from, steps);
+    }
   }
 
   // Q: lane n's row, eight elements a step
@@ -205,29 +373,15 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
     }
   }
 
-  const int c = lane % VPR, sub = lane / VPR;  // the 16-byte piece and row this lane stages
   const char* const kbase = (const char*)a.cache.base + g * a.cache.head_stride_bytes + (c < vecs ? c : 0) * 16;
   const int32_t* const table = a.batch.block_table + x.r * a.batch.bt_row_stride;
   const int cols = (int)a.batch.max_blocks_per_req;
-  char* const sk_put = sk + (w * KW + sub) * KROW + c * 16;
-  char* const sv_put = sv + (w * KW + sub) * VROW + c * 16;
-  const int kw = KEYS ? w * KW : 0;  // first slot of a tile that this wavefront computes
-  const char* const sk_get = sk + (kw + n) * KROW + hf * 16;
-  const char* const sv_get = sv + (kw + 4 * hf + ((lane & 15) >> 2)) * VROW + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-  if (vecs < VPR && c >= vecs) {  // the padding of every row is zero, once
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      *(u32x4*)(sk_put + i * RPI * KROW) = u32x4{0, 0, 0, 0};
-      *(u32x4*)(sv_put + i * RPI * VROW) = u32x4{0, 0, 0, 0};
-    }
-  }
 
   f32x16 acc[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) acc[d] = f32x16{};
   float m = -INFINITY, l = 0;
   const float c1 = a.scale * kLog2e;
-  int errs = 0;
 
   // staging: lane l looks up slot l % KW of the wavefront's share of a tile
   auto load_id = [&](int t) -> int32_t {
@@ -254,10 +408,15 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   };
 
   int32_t id = 0;
+  tb = uniform(tb);
+  te = uniform(te);
   if (tb < te) {
     fetch(tb, load_id(tb));
     id = load_id(tb + 1);
   }
+  // Q is here before the loop: a wait for it inside would be one for the loads in flight as well
+#pragma unroll
+  for (int st = 0; st < KSTEPS; ++st) asm volatile("" : "+v"(q[st]));
   for (int t = tb; t < te; ++t) {
     const int k0 = t * BN;
     // every row sees every slot of an inner tile
@@ -395,7 +554,6 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
     if constexpr (KEYS) __builtin_amdgcn_wave_barrier();
     else lds_barrier();
   }
-  if (errs) raise(a.err, errs);
   l += other_half(l);
 
   if constexpr (KEYS) {
@@ -442,122 +600,193 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
     }
   }
 
-  if (!used) return;
+  const AttendArgs end = argument<AttendArgs>();
+  const bool whole = !SHARED || (from == 0 && to == steps);
   const float inv = l == 0 ? 0.0f : 1.0f / l;
-  const int64_t flat = q_row * a.num_heads + head;
+  // where a part's row goes: share index of tile tile0 + x.tile
+  const int64_t part = ((int64_t)(index + tile0 + x.tile) * end.cache.num_kv_heads + g) * ROWS + (row - row0);
   constexpr int QUADS = KEYS ? 1 : 4;  // register quads of each 32 dimensions that this lane stores
 #pragma unroll
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int i = 0; i < QUADS; ++i) {
       const int e = d * 32 + 8 * (KEYS ? w : i) + 4 * hf;
-      if (e >= a.cache.head_dim) continue;
+      if (!used || e >= end.cache.head_dim) continue;
       f32x4 v;
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = l == 0 ? 0.0f : acc[d][4 * i + k] * inv;
-      if (sp.count > 1) {
-        gstore(sp.acc + (split * sp.rows + flat) * a.cache.head_dim + e, v);
+      if (SHARED && !whole) {
+        gstore(sp.acc + part * end.cache.head_dim + e, v);
       } else {
-        gstore((char*)a.out.base + q_row * a.out.token_stride + head * a.out.head_stride + e * 2,
+        gstore((char*)end.out.base + q_row * end.out.token_stride + head * end.out.head_stride + e * 2,
                __builtin_convertvector(v, typename E::V4));
       }
     }
-  if (hf == 0 && (!KEYS || w == 0)) {
+  if (used && hf == 0 && (!KEYS || w == 0)) {
     const float lse2 = l == 0 ? -INFINITY : m + __builtin_amdgcn_logf(l);
-    if (sp.count > 1) sp.lse[split * sp.rows + flat] = lse2;
-    else if (a.lse) a.lse[flat] = lse2 * kLn2;
+    if (SHARED && !whole) sp.lse[part] = lse2;
+    else if (end.lse) end.lse[q_row * end.num_heads + head] = lse2 * kLn2;
   }
+
+  if constexpr (!SHARED) break;
+  left -= to - from;
+  if (left <= 0) break;
+  // the next tile, of this request or of the next one that has any
+  from = 0;
+  if (++x.tile == tiles) {
+    tile0 += tiles;
+    do {
+      x = request_uniform(a, x.r + 1, cap);
+      extent<ROWS, BN>(a, x, group, &tiles, &steps);
+      tiles = uniform(tiles);
+      steps = uniform(steps);
+    } while (tiles == 0);
+  }
+  if constexpr (KEYS) {
+    __syncthreads();  // the join above has used the tiles' LDS
+    clear_padding();
+  }
+  }
+  if (errs) raise(a.err, errs);
 }
 
-// Joins the parts of split contexts: out = sum_s 2^(lse_s - top) o_s / sum_s 2^(lse_s - top). A thread takes
-// four dimensions of one row and every PG-th part, PG threads a row and dimension: with few rows the
-// parts are read side by side (64 parts of 32 rows: 65 -> 6 us). Parts that saw nothing are not read.
-template <class E, int PG>
+// Joins the parts of a tile: out = sum_s 2^(lse_s - top) o_s / sum_s 2^(lse_s - top). A thread takes four
+// dimensions of one row, and with many parts only every fourth or eighth of them, the threads of a row and
+// dimension side by side. What bounds it is one chain of loads: the batch, then the parts.
+template <class E, int ROWS, int BN>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, Split sp) {
   __shared__ f32x4 sums[256];
   __shared__ float tops[256], totals[256];
-  const int quads = a.cache.head_dim / 4, per = 256 / PG;
-  const int tid = threadIdx.x, pg = tid / per;
-  const int64_t i = (int64_t)blockIdx.x * per + tid % per, flat = i / quads;
-  const int64_t t = flat / a.num_heads;
-  const bool used = flat < sp.rows && t >= a.batch.q_offsets[0] && t < a.batch.q_offsets[a.batch.num_reqs];
-  const int e = (int)(i - flat * quads) * 4;
-  float top = -INFINITY, total = 0;
-  f32x4 o = {};
-  if (used) {
-    for (int s = pg; s < sp.count; s += PG) top = fmaxf(top, sp.lse[s * sp.rows + flat]);
-    const float ref = top == -INFINITY ? 0.0f : top;
-#pragma unroll 4
-    for (int s = pg; s < sp.count; s += PG) {
-      const float lse = sp.lse[s * sp.rows + flat];
-      if (lse == -INFINITY) continue;
-      const float wgt = __builtin_amdgcn_exp2f(lse - ref);
-      total += wgt;
-      o += wgt * gload<f32x4>(sp.acc + (s * sp.rows + flat) * a.cache.head_dim + e);
-    }
-  }
-  if constexpr (PG > 1) {
-    sums[tid] = o;
-    tops[tid] = top;
-    totals[tid] = total;
-    __syncthreads();
-    if (pg) return;
+  const int group = a.num_heads / a.cache.num_kv_heads, quads = a.cache.head_dim / 4;
+  const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int g = blockIdx.x % a.cache.num_kv_heads, tile = blockIdx.x / a.cache.num_kv_heads;
+  Shares all;
+  const Requests q = locate<ROWS, BN>(a, group, cap, lane, sp.shares, &all, [&](const Shares&, const Requests& q) {
+    return q.tile0 <= tile && tile < q.tile0 + q.tiles;
+  });
+  if (q.steps == 0) return;  // no such tile
+  const int64_t begin = q.step0 + (int64_t)(tile - q.tile0) * q.steps;
+  const int s_from = share_of(all, begin), s_to = share_of(all, begin + q.steps - 1) + 1;
+  if (s_to - s_from == 1) return;  // one share computed it whole
+  Rows x = q.x;
+  x.tile = tile - q.tile0;
+  const int rows = x.tokens * group - x.tile * ROWS, items = (rows < ROWS ? rows : ROWS) * quads;
+  const int ways_log = s_to - s_from <= 3 ? 0 : s_to - s_from <= 16 ? 2 : 3;
+  const int ways = 1 << ways_log, per = 256 >> ways_log, way = tid >> (8 - ways_log);
+  for (int at = blockIdx.y * per; at < items; at += gridDim.y * per) {
+    const int item = at + (tid & (per - 1)), row = item / quads, e = (item - row * quads) * 4;
+    const bool used = item < items;
+    auto part = [&](int s) { return ((int64_t)(s + tile) * a.cache.num_kv_heads + g) * ROWS + row; };
+    float top = -INFINITY, total = 0;
+    f32x4 o = {};
+    if (used) {
+      for (int s0 = s_from + way; s0 < s_to; s0 += 4 * ways) {
+        float lse[4];
+        f32x4 v[4];
 #pragma unroll
-    for (int k = 1; k < PG; ++k) top = fmaxf(top, tops[k * per + tid]);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    total = 0;
-    o = f32x4{};
+        for (int k = 0; k < 4; ++k) {  // four parts side by side, the last one again where there are fewer
+          const int s = s0 + k * ways < s_to ? s0 + k * ways : s0;
+          lse[k] = gload<float>(sp.lse + part(s));
+          v[k] = gload<f32x4>(sp.acc + part(s) * a.cache.head_dim + e);
+          if (s0 + k * ways >= s_to) lse[k] = -INFINITY;
+        }
+        const float m = fmaxf(fmaxf(fmaxf(lse[0], lse[1]), fmaxf(lse[2], lse[3])), top);
+        const float ref = m == -INFINITY ? 0.0f : m, keep = __builtin_amdgcn_exp2f(top - ref);
+        total *= keep;
+        o *= keep;
 #pragma unroll
-    for (int k = 0; k < PG; ++k) {
-      const float m = tops[k * per + tid];
-      if (m == -INFINITY) continue;
-      const float wgt = __builtin_amdgcn_exp2f(m - ref);
-      total += wgt * totals[k * per + tid];
-      o += wgt * sums[k * per + tid];
+        for (int k = 0; k < 4; ++k) {
+          const float wgt = __builtin_amdgcn_exp2f(lse[k] - ref);
+          total += wgt;
+          if (lse[k] != -INFINITY) o += wgt * v[k];
+        }
+        top = m;
+      }
     }
+    if (ways > 1) {
+      __syncthreads();
+      sums[tid] = o;
+      tops[tid] = top;
+      totals[tid] = total;
+      __syncthreads();
+      if (way) continue;
+      for (int k = 1; k < ways; ++k) top = fmaxf(top, tops[k * per + tid]);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      total = 0;
+      o = f32x4{};
+      for (int k = 0; k < ways; ++k) {
+        const float m = tops[k * per + tid];
+        if (m == -INFINITY) continue;
+        const float wgt = __builtin_amdgcn_exp2f(m - ref);
+        total += wgt * totals[k * per + tid];
+        o += wgt * sums[k * per + tid];
+      }
+    }
+    if (!used) continue;
+    const int flat = x.tile * ROWS + row, token = flat / group, head = g * group + flat - token * group;
+    const int64_t t = x.q0 + token;
+    const float inv = total == 0 ? 0.0f : 1.0f / total;
+    gstore((char*)a.out.base + t * a.out.token_stride + head * a.out.head_stride + e * 2,
+           __builtin_convertvector(o * inv, typename E::V4));
+    if (e == 0 && a.lse)
+      a.lse[t * a.num_heads + head] = total == 0 ? -INFINITY : (top + __builtin_amdgcn_logf(total)) * kLn2;
   }
-  if (!used) return;
-  const float inv = total == 0 ? 0.0f : 1.0f / total;
-  gstore((char*)a.out.base + t * a.out.token_stride + (flat - t * a.num_heads) * a.out.head_stride + e * 2,
-         __builtin_convertvector(o * inv, typename E::V4));
-  if (e == 0 && a.lse) a.lse[flat] = total == 0 ? -INFINITY : (top + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
 // The launch shape of a batch: by slots (KEYS) where a request's rows of one KV head fit one tile of
-// 32, and as many parts of the contexts as fill the GPU with two workgroups a CU, each at least
-// kMinPart slots long.
-constexpr int kMinPart = 512, kMaxParts = 64, kFill = 512;
+// 32. Where the tiles alone do not fill the GPU with two workgroups a CU (kFill), or leave a decode
+// batch's uneven contexts to a few rounds of workgroups, they are shared out evenly to kFill
+// workgroups, of kMinSteps steps at least, if there is a workspace for the parts.
+constexpr int kFill = 512, kMinSteps = 4;
+constexpr int64_t kMaxContext = 0x7fffffff;
 
 struct Plan {
   bool keys;
-  int32_t tiles, parts;
+  int32_t tiles, shares;
 };
 Plan plan_attention(const kvx_paged_cache& c, const kvx_batch& b, int32_t num_heads) {
   const int64_t group = num_heads / c.num_kv_heads;
   const int64_t longest = b.max_query_len < b.num_tokens ? b.max_query_len : b.num_tokens;
   Plan p;
   p.keys = longest * group <= 32;
-  const int64_t rows = p.keys ? 32 : 128;
+  const int64_t rows = p.keys ? 32 : 128, slots = p.keys ? 128 : 64;
   p.tiles = (int32_t)(b.num_tokens * group / rows + b.num_reqs);
   int64_t busy = b.num_reqs * ((longest * group + rows - 1) / rows);
   if (busy > p.tiles) busy = p.tiles;
-  busy = (busy > 0 ? busy : 1) * c.num_kv_heads;
-  int64_t parts = kFill / busy;
-  if (parts > b.max_context_len / kMinPart) parts = b.max_context_len / kMinPart;
-  if (parts > kMaxParts) parts = kMaxParts;
-  p.parts = parts > 1 ? (int32_t)parts : 1;
+  if (busy < 1) busy = 1;
+  const int64_t context = b.max_context_len < kMaxContext ? b.max_context_len : kMaxContext;
+  int64_t shares = kFill / c.num_kv_heads, most = busy * (context / slots) / kMinSteps;
+  if (shares > most) shares = most;
+  const bool uneven = busy * c.num_kv_heads < (p.keys ? 4 * kFill : kFill);
+  p.shares = uneven && shares > (p.keys ? busy / 4 : busy) ? (int32_t)shares : 0;
   return p;
 }
 
-int64_t part_bytes(const kvx_paged_cache& c, const kvx_batch& b, int32_t num_heads) {
-  return b.num_tokens * num_heads * 4 * ((int64_t)c.head_dim + 4);
+// Bytes of a slot: a part of one tile of every KV head.
+int64_t slot_bytes(const kvx_paged_cache& c, bool keys) {
+  return (int64_t)c.num_kv_heads * (keys ? 32 : 128) * 4 * ((int64_t)c.head_dim + 1);
 }
 
 template <class E, int DP>
 void launch_attend(const AttendArgs& a, BlockDiv div, const Split& sp, bool keys, hipStream_t stream) {
-  const dim3 grid((unsigned)(sp.tiles * a.cache.num_kv_heads), sp.count);
-  if (keys) attend_kernel<E, DP, true><<<grid, 256, 0, stream>>>(a, div, sp);
-  else attend_kernel<E, DP, false><<<grid, 256, 0, stream>>>(a, div, sp);
+  const int heads = a.cache.num_kv_heads;
+  if (sp.shares == 0) {
+    const dim3 grid((unsigned)(sp.tiles * heads));
+    if (keys) attend_kernel<E, DP, true, false><<<grid, 256, 0, stream>>>(a, div, sp);
+    else attend_kernel<E, DP, false, false><<<grid, 256, 0, stream>>>(a, div, sp);
+    return;
+  }
+  const dim3 grid((unsigned)(sp.shares * heads));
+  const int64_t blocks = (int64_t)sp.tiles * heads;
+  const dim3 join((unsigned)blocks, blocks >= 4096 ? 1u : (unsigned)(4096 / blocks < 16 ? 4096 / blocks : 16));
+  if (keys) {
+    attend_kernel<E, DP, true, true><<<grid, 256, 0, stream>>>(a, div, sp);
+    join_kernel<E, 32, 128><<<join, 256, 0, stream>>>(a, sp);
+  } else {
+    attend_kernel<E, DP, false, true><<<grid, 256, 0, stream>>>(a, div, sp);
+    join_kernel<E, 128, 64><<<join, 256, 0, stream>>>(a, sp);
+  }
 }
 
 template <class E>
@@ -565,11 +794,6 @@ void launch_attend_dims(const AttendArgs& a, BlockDiv div, const Split& sp, bool
   if (a.cache.head_dim <= 64) launch_attend<E, 64>(a, div, sp, keys, stream);
   else if (a.cache.head_dim <= 128) launch_attend<E, 128>(a, div, sp, keys, stream);
   else launch_attend<E, 256>(a, div, sp, keys, stream);
-  if (sp.count > 1) {
-    const int64_t threads = sp.rows * (a.cache.head_dim / 4);
-    if (sp.count <= 4) join_kernel<E, 1><<<dim3((unsigned)((threads + 255) / 256)), 256, 0, stream>>>(a, sp);
-    else join_kernel<E, 8><<<dim3((unsigned)((threads + 31) / 32)), 256, 0, stream>>>(a, sp);
-  }
 }
 
 // --------------------------------------------------------------------------------------
@@ -583,11 +807,8 @@ struct MassRows {
 };
 __device__ __forceinline__ bool mass_rows(const MassArgs& ma, int r, int group, int64_t cap, MassRows* m) {
   const AttendArgs& a = ma.at;
-  Rows& x = m->x;
-  x.r = r;
-  x.q0 = clamp64(a.batch.q_offsets[r], 0, a.batch.num_tokens);
-  x.tokens = (int32_t)(clamp64(a.batch.q_offsets[r + 1], x.q0, a.batch.num_tokens) - x.q0);
-  x.context = a.cache.num_blocks > 0 ? (int32_t)clamp64(a.batch.context_lens[r], 0, cap) : 0;
+  m->x = request(a, r, cap);
+  const Rows& x = m->x;
   if (x.context > ma.mass_width && blockIdx.y == 0) raise(a.err, KVX_DEVERR_TABLE_RANGE);
   if (x.tokens == 0) return false;
   m->rows = x.tokens * group;
@@ -829,6 +1050,10 @@ __global__ __launch_bounds__(256, DP <= 128 ? 3 : 2) void mass_few_kernel(MassAr
       load_k(from, look_up(from));
       int32_t id = from + 128 < to ? look_up(from + 128) : -1;
       load_rows(row0);
+      // here before the loop: a wait for them inside would be one for the loads in flight as well
+#pragma unroll
+      for (int st = 0; st < KSTEPS; ++st) asm volatile("" : "+v"(q[st]));
+      asm volatile("" : "+v"(ref));
       for (int k0 = from; k0 < to; k0 += 128) {
         const bool store = ok;
         const float old = before;
@@ -891,12 +1116,13 @@ void launch_mass_dims(const MassArgs& m, BlockDiv div, dim3 grid, int span, hipS
 
 hipError_t launch_attention(const AttendArgs& a, hipStream_t stream) {
   const Plan p = plan_attention(a.cache, a.batch, a.num_heads);
-  Split sp = {p.parts, p.tiles, a.cache.num_kv_heads, nullptr, nullptr, a.batch.num_tokens * a.num_heads};
-  const int64_t fit = a.workspace_bytes / part_bytes(a.cache, a.batch, a.num_heads);
-  if (sp.count > fit) sp.count = fit > 1 ? (int32_t)fit : 1;
-  if (sp.count > 1) {
+  Split sp = {p.shares, p.tiles, nullptr, nullptr};
+  // a workspace too small for the plan takes fewer shares, as long as they are worth it
+  const int64_t fit = a.workspace_bytes / slot_bytes(a.cache, p.keys) - p.tiles;
+  if (sp.shares > fit) sp.shares = fit > 1 ? (int32_t)fit : 0;
+  if (sp.shares > 0) {
     sp.acc = (float*)a.workspace;  // first: rows of 16-byte vectors
-    sp.lse = sp.acc + sp.count * sp.rows * a.cache.head_dim;
+    sp.lse = sp.acc + (int64_t)(sp.shares + p.tiles) * a.cache.num_kv_heads * (p.keys ? 32 : 128) * a.cache.head_dim;
   }
   const BlockDiv div = block_div(a.cache.block_size);
   if (a.cache.dtype == KVX_DTYPE_BF16) launch_attend_dims<Bf16>(a, div, sp, p.keys, stream);
@@ -906,7 +1132,7 @@ hipError_t launch_attention(const AttendArgs& a, hipStream_t stream) {
 
 int64_t attention_workspace(const kvx_paged_cache& c, const kvx_batch& b, int32_t num_heads) {
   const Plan p = plan_attention(c, b, num_heads);
-  return p.parts > 1 ? p.parts * part_bytes(c, b, num_heads) : 0;
+  return p.shares > 0 ? (p.shares + (int64_t)p.tiles) * slot_bytes(c, p.keys) : 0;
 }
 
 hipError_t launch_mass(const MassArgs& m, hipStream_t stream) {
