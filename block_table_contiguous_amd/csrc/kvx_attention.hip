@@ -243,6 +243,9 @@ __device__ __forceinline__ int here(int x) {
   return x;
 }
 
+// Kinds of instructions for __builtin_amdgcn_sched_group_barrier.
+constexpr int kMfma = 0x8, kDsRead = 0x100, kVector = 0x402;
+
 // Barrier for data passed through LDS: global loads stay in flight across it.
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -467,6 +470,14 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
       for (int st = 0; st < KSTEPS; ++st)
         s[kt] = mfma(E(), *(const u32x4*)(sk_get + kt * 32 * KROW + st * 32), q[st], s[kt]);
     }
+    // K is read eight pieces ahead of the products: read as they are needed, each would wait for LDS
+    __builtin_amdgcn_sched_group_barrier(kDsRead, 8, 0);
+#pragma unroll
+    for (int i = 0; i < KT * KSTEPS - 8; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(kMfma, 8, 0);
     if (!inner || ~there) {
       const int at = here(k0 + kw + 4 * hf), lo = see.x - at, hi = see.y - at;
 #pragma unroll
@@ -498,31 +509,43 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
         for (int i = 0; i < 16; ++i) acc[d][i] *= shrink;
     }
     const float ref = m == -INFINITY ? 0.0f : m;
+    // Weights and products by 16 slots: V is read one group ahead, and the weights of a group are
+    // formed in the shadow of the products of the one before. The wavefront that is here goes first: the
+    // SIMD's other one does its own part better while these products run (1177 -> 1125 us at 2048
+    // queries of 32 heads over 32768 slots).
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+    for (int gr = 0; gr < 2 * KT; ++gr) {
+      f32x8 pv;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[kt][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][i], c1, -ref));
-        l += s[kt][i];
+      for (int i = 0; i < 8; ++i) {
+        const int at = 8 * (gr % 2) + i;
+        pv[i] = s[gr / 2][at] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[gr / 2][at], c1, -ref));
+        l += pv[i];
       }
+      // one rounding of each weight to the element type, which the matrix unit takes
+      const u32x4 p = narrow<E>(pv);
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        f32x8 pv;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) pv[i] = s[kt][8 * h + i];
-        // one rounding of each weight to the element type, which the matrix unit takes
-        const u32x4 p = narrow<E>(pv);
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const char* at = sv_get + (kt * 32 + 16 * h) * VROW + d * 64;
-          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KVX_LDS s16x4*)at);
-          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KVX_LDS s16x4*)(at + 8 * VROW));
-          const s16x8 va = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-          acc[d] = mfma(E(), __builtin_bit_cast(u32x4, va), p, acc[d]);
-        }
+      for (int d = 0; d < DT; ++d) {
+        const char* at = sv_get + 16 * gr * VROW + d * 64;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KVX_LDS s16x4*)at);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KVX_LDS s16x4*)(at + 8 * VROW));
+        const s16x8 va = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        acc[d] = mfma(E(), __builtin_bit_cast(u32x4, va), p, acc[d]);
       }
+    }
+    __builtin_amdgcn_sched_group_barrier(kDsRead, 2 * DT, 1);
+    __builtin_amdgcn_sched_group_barrier(kVector, 28, 1);
+#pragma unroll
+    for (int gr = 0; gr < 2 * KT; ++gr) {
+      if (gr + 1 < 2 * KT) __builtin_amdgcn_sched_group_barrier(kDsRead, 2 * DT, 1);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 1);
+        if (gr + 1 < 2 * KT) __builtin_amdgcn_sched_group_barrier(kVector, 28 / DT, 1);
+      }
+    }
+    __builtin_amdgcn_s_setprio(0);
     if (skipped) {
       for (uint64_t todo = skipped; todo; todo &= todo - 1) {
         const int o = __builtin_ctzll(todo), j = k0 + kw + o;
