@@ -243,6 +243,13 @@ __device__ __forceinline__ int here(int x) {
   return x;
 }
 
+// A buffer that starts at p (the same in all lanes) for loads whose offsets the caller keeps inside
+// the memory: a scalar base, a scalar step and a lane's constant offset make an address for nothing.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const char* p) {
+  const uint64_t at = (uint64_t)uniform((int64_t)p);
+  return __builtin_amdgcn_make_buffer_rsrc((void*)at, 0, 0x7fffffff, 0x00027000);
+}
+
 // Kinds of instructions for __builtin_amdgcn_sched_group_barrier.
 constexpr int kMfma = 0x8, kDsRead = 0x100, kVector = 0x402;
 
@@ -276,7 +283,7 @@ struct Split {
 // K and V go from memory to registers one tile ahead and then to LDS, in rows padded so that the reads of
 // 16 rows (K: 16 bytes a row), or of 4 slots x 64 bytes (V: 64 bytes a row), fall on different banks;
 // padding, unlike a swizzle, leaves every address one register and a constant.
-template <class E, int DP, bool KEYS, bool SHARED>
+template <class E, int DP, bool KEYS, bool BY_BLOCK, bool SHARED>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendArgs args, BlockDiv div, Split sp) {
   const AttendArgs a = argument<AttendArgs>();
   constexpr int ROWS = KEYS ? 32 : 128, BN = KEYS ? 128 : 64, KW = BN / 4;
@@ -337,6 +344,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
     if ((int64_t)x.tile * ROWS >= (int64_t)x.tokens * group) return;
   }
   int errs = 0;
+  bool bad_blocks = false;
   for (;;) {
   const AttendArgs a = argument<AttendArgs>();
   if constexpr (SHARED) to = from + left < steps ? (int)(from + left) : steps;
@@ -386,7 +394,11 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   float m = -INFINITY, l = 0;
   const float c1 = a.scale * kLog2e;
 
-  // staging: lane l looks up slot l % KW of the wavefront's share of a tile
+  // Staging. BY_BLOCK, where 16 slots always lie in one block: their rows are token_stride apart, and the block
+  // is looked up and the rows' addresses formed once a wavefront, in scalar registers. Otherwise lane
+  // l looks up slot l % KW of the wavefront's share and passes the row's offset on.
+  constexpr int BLKS = KW / 16;
+  const uint32_t v_off = (uint32_t)(sub * (int32_t)a.cache.token_stride_bytes) + (c < vecs ? c : 0) * 16;
   auto load_id = [&](int t) -> int32_t {
     const int b = block_of(div, t * BN + w * KW + lane % KW);
     return gload<int32_t>(table + (b < cols ? b : cols - 1));
@@ -394,10 +406,39 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   u32x4 rk[NI], rv[NI];
   uint64_t ok_mask = 0;
   auto fetch = [&](int t, int32_t id) {
+    // a slot that is not there is read from the cache's first rows and then set to zero
+    if constexpr (BY_BLOCK) {
+      ok_mask = 0;
+#pragma unroll
+      for (int k = 0; k < BLKS; ++k) {
+        const int32_t block = lane_of(id, k * 16);
+        const int j = t * BN + w * KW + k * 16;
+        int there = kend - j < 16 ? kend - j : 16;
+        if (there < 0) there = 0;
+        int64_t off = 0;
+        if ((uint32_t)block < (uint64_t)a.cache.num_blocks) {
+          off = block * a.cache.block_stride_bytes +
+                (int64_t)(j - block_of(div, j) * div.size) * a.cache.token_stride_bytes;
+          ok_mask |= (uint64_t)((1u << there) - 1) << (k * 16);
+        } else if (there > 0) {
+          bad_blocks = true;
+        }
+        const char* p = (const char*)a.cache.base + g * a.cache.head_stride_bytes + off;
+        const auto kr = rows_at(p), vr = rows_at(p + a.cache.kv_stride_bytes);
+#pragma unroll
+        for (int i = 0; i < NI / BLKS; ++i) {
+          const int down = i * RPI * (int32_t)a.cache.token_stride_bytes;
+          rk[k * (NI / BLKS) + i] = __builtin_amdgcn_raw_buffer_load_b128(kr, v_off, down, 0);
+          rv[k * (NI / BLKS) + i] = __builtin_amdgcn_raw_buffer_load_b128(vr, v_off, down, 0);
+        }
+      }
+      ok_mask |= ok_mask << 32;  // lanes l and l + 32 stand for the same slot
+      if (KW == 16) ok_mask |= ok_mask << 16;
+      return;
+    } else {
     const int j = t * BN + w * KW + lane % KW;
     const bool in = j < kend, ok = in && (uint32_t)id < (uint64_t)a.cache.num_blocks;
     if (in && !ok) errs |= KVX_DEVERR_BLOCK_RANGE;
-    // a slot that is not there is read from the cache's first row and then set to zero
     const int64_t off = ok ? id * a.cache.block_stride_bytes +
                                  (int64_t)(j - block_of(div, j) * div.size) * a.cache.token_stride_bytes
                            : 0;
@@ -407,6 +448,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
       const char* p = kbase + __shfl(off, i * RPI + sub);
       rk[i] = gload<u32x4>(p);
       rv[i] = gload<u32x4>(p + a.cache.kv_stride_bytes);
+    }
     }
   };
 
@@ -670,6 +712,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
     clear_padding();
   }
   }
+  if (bad_blocks) errs |= KVX_DEVERR_BLOCK_RANGE;
   if (errs) raise(a.err, errs);
 }
 
@@ -794,20 +837,25 @@ int64_t slot_bytes(const kvx_paged_cache& c, bool keys) {
 template <class E, int DP>
 void launch_attend(const AttendArgs& a, BlockDiv div, const Split& sp, bool keys, hipStream_t stream) {
   const int heads = a.cache.num_kv_heads;
+  // Blocks of a multiple of 16 tokens, as they usually are: addresses by block, which spares the vector unit (a
+  // long chunk 1125 -> 1081 us). The decode kernel waits for memory instead, and is faster without (138 against 148 us).
+  const bool by_block = a.cache.block_size % 16 == 0 && a.cache.token_stride_bytes <= (1 << 24);
   if (sp.shares == 0) {
     const dim3 grid((unsigned)(sp.tiles * heads));
-    if (keys) attend_kernel<E, DP, true, false><<<grid, 256, 0, stream>>>(a, div, sp);
-    else attend_kernel<E, DP, false, false><<<grid, 256, 0, stream>>>(a, div, sp);
+    if (keys) attend_kernel<E, DP, true, false, false><<<grid, 256, 0, stream>>>(a, div, sp);
+    else if (by_block) attend_kernel<E, DP, false, true, false><<<grid, 256, 0, stream>>>(a, div, sp);
+    else attend_kernel<E, DP, false, false, false><<<grid, 256, 0, stream>>>(a, div, sp);
     return;
   }
   const dim3 grid((unsigned)(sp.shares * heads));
   const int64_t blocks = (int64_t)sp.tiles * heads;
   const dim3 join((unsigned)blocks, blocks >= 4096 ? 1u : (unsigned)(4096 / blocks < 16 ? 4096 / blocks : 16));
   if (keys) {
-    attend_kernel<E, DP, true, true><<<grid, 256, 0, stream>>>(a, div, sp);
+    attend_kernel<E, DP, true, false, true><<<grid, 256, 0, stream>>>(a, div, sp);
     join_kernel<E, 32, 128><<<join, 256, 0, stream>>>(a, sp);
   } else {
-    attend_kernel<E, DP, false, true><<<grid, 256, 0, stream>>>(a, div, sp);
+    if (by_block) attend_kernel<E, DP, false, true, true><<<grid, 256, 0, stream>>>(a, div, sp);
+    else attend_kernel<E, DP, false, false, true><<<grid, 256, 0, stream>>>(a, div, sp);
     join_kernel<E, 128, 64><<<join, 256, 0, stream>>>(a, sp);
   }
 }
