@@ -56,6 +56,7 @@ class PagedCache(ctypes.Structure):
     _fields_ = [("base", _P), ("num_blocks", _I64), ("block_stride_bytes", _I64), ("token_stride_bytes", _I64),
                 ("kv_stride_bytes", _I64), ("head_stride_bytes", _I64), ("block_size", _I32), ("num_kv_heads", _I32),
                 ("head_dim", _I32), ("dtype", _I32)]
+    tensor = None  # the tensor that it describes
 
 
 class Batch(ctypes.Structure):
@@ -582,90 +583,107 @@ def _torch_int64():
 # ---------------------------------------------------------------------------------------
 # calls that compute on a paged cache (include/kvx_attention.h)
 # ---------------------------------------------------------------------------------------
+# A decode step makes a few of these calls a layer, so the checks read each shape and stride once.
 
-def _step(t, dim: int) -> int:
-    """Stride of a dimension in elements; 0 where it has at most one entry and is never stepped."""
-    return t.stride(dim) if t.shape[dim] > 1 else 0
-
-
-def _dtype_code(t, name: str) -> int:
-    import torch
-
-    if t.dtype == torch.bfloat16:
-        return DTYPE_BF16
-    if t.dtype == torch.float16:
-        return DTYPE_FP16
-    raise TypeError(f"kvx: {name} must be bfloat16 or float16, got {t.dtype}")
+_ELEMENTS = {}  # torch element type -> DTYPE_*, filled on first use
+_device_query = None  # as _raw_stream: torch's internal query of the current device, if it is there
 
 
-def _on_current_device(*tensors):
+def _dtype_code(dtype, name: str) -> int:
+    if not _ELEMENTS:
+        import torch
+
+        _ELEMENTS.update({torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16})
+    code = _ELEMENTS.get(dtype)
+    if code is None:
+        raise TypeError(f"kvx: {name} must be bfloat16 or float16, got {dtype}")
+    return code
+
+
+def _current_device() -> int:
+    global _device_query
+    if _device_query is None:
+        import torch
+
+        query = getattr(torch._C, "_cuda_getDevice", None)
+        _device_query = query if query is not None and query() == torch.cuda.current_device() \
+            else torch.cuda.current_device
+    return _device_query()
+
+
+def _on_current_device(tensors):
     """Every tensor given lives on the current device, whose stream the call is enqueued on."""
-    import torch
-
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError("kvx: tensors must live on the GPU")
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != here:
-            raise ValueError("kvx: every tensor must live on the current device")
+    where = {t.get_device() for t in tensors if t is not None}
+    if min(where) < 0:
+        raise ValueError("kvx: tensors must live on the GPU")
+    if where != {_current_device()}:
+        raise ValueError("kvx: every tensor must live on the current device")
 
 
 def paged_cache(kv_cache, layout: str = "blocks_tokens_kv") -> PagedCache:
     """A 5-D cache tensor (one of cache_strides' layouts, any strides whose last dimension is
     dense) as the struct that the calls below take. They make it from the tensor themselves; a
-    caller that makes the same call many times can make it once and pass it with the tensor kept
-    alive."""
-    if kv_cache.dim() != 5 or kv_cache.shape[{"blocks_tokens_kv": 2, "blocks_kv_tokens": 1}.get(layout, 0)] != 2:
+    caller that makes the same call many times can make it once and pass it instead."""
+    shape, stride = kv_cache.shape, kv_cache.stride()
+    b, o, w = {"blocks_tokens_kv": (0, 1, 2), "blocks_kv_tokens": (0, 2, 1), "kv_blocks_tokens": (1, 2, 0)}.get(
+        layout, (0, 0, 0))
+    if b == o:
+        raise ValueError(f"unknown layout {layout}")
+    if len(shape) != 5 or shape[w] != 2:
         raise ValueError("kvx: kv_cache must be a 5-D cache tensor of the given layout")
-    code = _dtype_code(kv_cache, "kv_cache")
-    nb, bs, block, token, kv = cache_strides(kv_cache, layout)
-    if kv_cache.shape[4] > 1 and kv_cache.stride(4) != 1:
+    code = _dtype_code(kv_cache.dtype, "kv_cache")
+    if shape[4] > 1 and stride[4] != 1:
         raise ValueError("kvx: the last dimension of kv_cache must be dense")
-    c = PagedCache(kv_cache.data_ptr(), nb, block if nb > 1 else 0, token if bs > 1 else 0, kv,
-                   _step(kv_cache, 3) * 2, bs, kv_cache.shape[3], kv_cache.shape[4], code)
-    c.tensor = kv_cache
+    # the stride of a dimension with one entry is never used and may be anything
+    c = PagedCache(kv_cache.data_ptr(), shape[b], 2 * stride[b] if shape[b] > 1 else 0,
+                   2 * stride[o] if shape[o] > 1 else 0, 2 * stride[w], 2 * stride[3] if shape[3] > 1 else 0, shape[o],
+                   shape[3], shape[4], code)
+    c.tensor = kv_cache  # kept alive, and looked at for its device
     return c
 
 
 def _cache(kv_cache, layout) -> PagedCache:
-    return kv_cache if isinstance(kv_cache, PagedCache) else paged_cache(kv_cache, layout)
+    return kv_cache if type(kv_cache) is PagedCache else paged_cache(kv_cache, layout)
 
 
-def _want_heads(t, tokens, heads, cache: PagedCache, name: str):
-    """A [tokens][heads][head_dim] tensor of the cache's element type, its last dimension dense
-    (heads None: any number)."""
-    if t.dim() != 3 or t.shape[0] != tokens or (heads is not None and t.shape[1] != heads) \
-            or t.shape[2] != cache.head_dim:
+def _rows(t, tokens: int, heads, cache: PagedCache, name: str):
+    """Byte strides (token, head) of a [tokens][heads][head_dim] tensor of the cache's element type,
+    its last dimension dense (heads None: any number)."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != tokens or (heads is not None and shape[1] != heads) or shape[2] != cache.head_dim:
         raise ValueError(f"kvx: {name} must be [num_tokens][heads][head_dim]")
-    if _dtype_code(t, name) != cache.dtype:
+    if _dtype_code(t.dtype, name) != cache.dtype:
         raise TypeError(f"kvx: {name} and kv_cache must have the same element type")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if stride[2] != 1 and shape[2] > 1:
         raise ValueError(f"kvx: the last dimension of {name} must be dense")
+    return 2 * stride[0] if shape[0] > 1 else 0, 2 * stride[1] if shape[1] > 1 else 0
 
 
-def _want_table(t, name="block_table"):
+def _table(t, reqs: int, name: str = "block_table"):
+    """(columns, row stride) of a block table with a row a request."""
     import torch
 
-    if t.dtype != torch.int32 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if t.dtype != torch.int32 or len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError(f"kvx: {name} must be a row-major int32 [num_reqs][width] tensor")
+    if shape[0] != reqs:
+        raise ValueError(f"kvx: {name} needs a row a request")
+    return shape[1], stride[0] if shape[0] > 1 else shape[1]
 
 
-def _row_stride(table) -> int:
-    return table.stride(0) if table.shape[0] > 1 else table.shape[1]
-
-
-def _want_lists(t, name: str, reqs: int, heads: Optional[int], width: Optional[int] = None):
-    """Float32 [num_reqs][heads][width], its last dimension dense."""
+def _lists(t, name: str, reqs: int, heads: Optional[int]):
+    """(request stride, head stride, width) of float32 [num_reqs][heads][width], the last dimension
+    dense."""
     import torch
 
+    shape, stride = t.shape, t.stride()
     if t.dtype != torch.float32:
         raise TypeError(f"kvx: {name} must be torch.float32, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != reqs or (heads is not None and t.shape[1] != heads) \
-            or (width is not None and t.shape[2] != width):
+    if len(shape) != 3 or shape[0] != reqs or (heads is not None and shape[1] != heads):
         raise ValueError(f"kvx: {name} must be [num_reqs][heads][width]")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if shape[2] > 1 and stride[2] != 1:
         raise ValueError(f"kvx: the last dimension of {name} must be dense")
+    return stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0, shape[2]
 
 
 def kvx_rope_and_cache(query, key, value, positions, inv_freq, pair_axis: Sequence[int], slot_mapping, kv_cache,
@@ -681,48 +699,49 @@ def kvx_rope_and_cache(query, key, value, positions, inv_freq, pair_axis: Sequen
     _want(positions, torch.int64, "positions")
     _want(inv_freq, torch.float32, "inv_freq")
     T = slot_mapping.numel()
-    if positions.dim() != 2 or positions.shape[1] != T:
+    axes = positions.shape
+    if len(axes) != 2 or axes[1] != T:
         raise ValueError("kvx: positions must be [num_axes][num_tokens]")
     pairs = len(pair_axis)
     if inv_freq.numel() != pairs:
         raise ValueError("kvx: pair_axis and inv_freq need one entry a pair")
     if (query is None) != (query_out is None):
         raise ValueError("kvx: query and query_out go together")
-    _want_heads(key, T, c.num_kv_heads, c, "key")
-    _want_heads(value, T, c.num_kv_heads, c, "value")
-    heads = 0
+    ks = _rows(key, T, c.num_kv_heads, c, "key")
+    vs = _rows(value, T, c.num_kv_heads, c, "value")
+    heads, qs, os_, q_ptr, o_ptr = 0, (0, 0), (0, 0), None, None
     if query is not None:
-        _want_heads(query, T, None, c, "query")
+        qs = _rows(query, T, None, c, "query")
         heads = query.shape[1]
-        _want_heads(query_out, T, heads, c, "query_out")
-    _on_current_device(query, key, value, positions, inv_freq, slot_mapping, getattr(c, "tensor", None), query_out,
-                       err_flag)
-    q, o = query if query is not None else key, query_out if query is not None else key
+        os_ = _rows(query_out, T, heads, c, "query_out")
+        q_ptr, o_ptr = query.data_ptr(), query_out.data_ptr()
+    _on_current_device((query, key, value, positions, inv_freq, slot_mapping, c.tensor, query_out, err_flag))
     st = _F["kvx_rope_and_cache"](
-        ctypes.byref(c), _ptr(query), _step(q, 0) * 2, _step(q, 1) * 2, heads, _ptr(key), _step(key, 0) * 2,
-        _step(key, 1) * 2, _ptr(value), _step(value, 0) * 2, _step(value, 1) * 2, T, _ptr(positions),
-        positions.shape[0], (_I32 * max(pairs, 1))(*pair_axis), _ptr(inv_freq), 2 * pairs, int(interleaved),
-        _ptr(slot_mapping), _ptr(query_out), _step(o, 0) * 2, _step(o, 1) * 2, _ptr(err_flag), _stream(stream))
+        c, q_ptr, *qs, heads, key.data_ptr(), *ks, value.data_ptr(), *vs, T, positions.data_ptr(), axes[0],
+        (_I32 * max(pairs, 1))(*pair_axis), inv_freq.data_ptr(), 2 * pairs, bool(interleaved), slot_mapping.data_ptr(),
+        o_ptr, *os_, _ptr(err_flag), _stream(stream))
     _check("kvx_rope_and_cache", st)
 
 
-def _batch(query, c: PagedCache, block_table, q_offsets, context_lens, max_query_len, max_context_len) -> Batch:
+def _batch(query, c: PagedCache, block_table, q_offsets, context_lens, max_query_len, max_context_len):
+    """(Batch, query heads, query strides)."""
     import torch
 
-    T, R = query.shape[0], context_lens.numel()
-    _want_heads(query, T, None, c, "query")
-    if query.shape[1] == 0 or query.shape[1] % c.num_kv_heads:
+    T, heads = query.shape[0], query.shape[1] if query.dim() == 3 else 0
+    qs = _rows(query, T, None, c, "query")
+    if heads == 0 or heads % c.num_kv_heads:
         raise ValueError("kvx: the query heads must be a multiple of the KV heads")
-    _want_table(block_table)
     _want(q_offsets, torch.int64, "q_offsets")
     _want(context_lens, torch.int64, "context_lens")
-    if block_table.shape[0] != R or q_offsets.numel() != R + 1:
-        raise ValueError("kvx: block_table needs a row a request and q_offsets num_reqs + 1 entries")
-    width = block_table.shape[1]
-    # plain addresses: _on_current_device checks the tensors before the call
-    return Batch(block_table.data_ptr(), q_offsets.data_ptr(), context_lens.data_ptr(), width,
-                 _row_stride(block_table), T, T if max_query_len is None else int(max_query_len),
-                 width * c.block_size if max_context_len is None else int(max_context_len), R)
+    R = context_lens.numel()
+    if q_offsets.numel() != R + 1:
+        raise ValueError("kvx: q_offsets needs num_reqs + 1 entries")
+    width, row = _table(block_table, R)
+    # plain addresses: _on_current_device looks at the tensors before the call
+    b = Batch(block_table.data_ptr(), q_offsets.data_ptr(), context_lens.data_ptr(), width, row, T,
+              T if max_query_len is None else int(max_query_len),
+              width * c.block_size if max_context_len is None else int(max_context_len), R)
+    return b, heads, qs
 
 
 def attention_workspace_bytes(query, kv_cache, num_reqs: int, max_query_len: int, max_context_len: int,
@@ -730,7 +749,7 @@ def attention_workspace_bytes(query, kv_cache, num_reqs: int, max_query_len: int
     """Bytes of workspace with which kvx_paged_attention splits such a batch as far as pays."""
     c = _cache(kv_cache, layout)
     b = Batch(None, None, None, 0, 0, query.shape[0], int(max_query_len), int(max_context_len), int(num_reqs))
-    n = _F["kvx_paged_attention_workspace"](ctypes.byref(c), ctypes.byref(b), query.shape[1])
+    n = _F["kvx_paged_attention_workspace"](c, b, query.shape[1])
     if n < 0:
         raise ValueError("kvx: kvx_paged_attention does not take a batch of these sizes")
     return int(n)
@@ -745,6 +764,14 @@ def new_attention_workspace(query, kv_cache, num_reqs: int, max_query_len: int, 
     return torch.empty(n, dtype=torch.uint8, device=query.device)
 
 
+def _want_lse(lse, T: int, heads: int):
+    import torch
+
+    _want(lse, torch.float32, "lse")
+    if tuple(lse.shape) != (T, heads):
+        raise ValueError("kvx: lse must be [num_tokens][heads]")
+
+
 def kvx_paged_attention(query, kv_cache, block_table, q_offsets, context_lens, out, lse=None,
                         scale: Optional[float] = None, causal: bool = True, window: int = 0,
                         max_query_len: Optional[int] = None, max_context_len: Optional[int] = None, workspace=None,
@@ -753,27 +780,20 @@ def kvx_paged_attention(query, kv_cache, block_table, q_offsets, context_lens, o
     [num_tokens][heads][head_dim]) over its paged cache of context_lens[r] slots, into out and,
     if given, lse (float32 [num_tokens][heads]). scale defaults to head_dim ** -0.5; max_query_len
     and max_context_len only choose the launch shape."""
-    import torch
-
     c = _cache(kv_cache, layout)
-    b = _batch(query, c, block_table, q_offsets, context_lens, max_query_len, max_context_len)
-    heads = query.shape[1]
-    _want_heads(out, query.shape[0], heads, c, "out")
+    b, heads, qs = _batch(query, c, block_table, q_offsets, context_lens, max_query_len, max_context_len)
+    os_ = _rows(out, b.num_tokens, heads, c, "out")
     if lse is not None:
-        _want(lse, torch.float32, "lse")
-        if lse.shape != query.shape[:2]:
-            raise ValueError("kvx: lse must be [num_tokens][heads]")
+        _want_lse(lse, b.num_tokens, heads)
     nbytes = 0
     if workspace is not None:
         if not workspace.is_contiguous():
             raise ValueError("kvx: workspace must be contiguous")
         nbytes = workspace.numel() * workspace.element_size()
-    _on_current_device(query, getattr(c, "tensor", None), block_table, q_offsets, context_lens, out, lse, workspace,
-                       err_flag)
+    _on_current_device((query, c.tensor, block_table, q_offsets, context_lens, out, lse, workspace, err_flag))
     st = _F["kvx_paged_attention"](
-        ctypes.byref(c), ctypes.byref(b), _ptr(query), _step(query, 0) * 2, _step(query, 1) * 2, heads,
-        c.head_dim ** -0.5 if scale is None else float(scale), int(causal), int(window), _ptr(out), _step(out, 0) * 2,
-        _step(out, 1) * 2, _ptr(lse), _ptr(workspace), nbytes, _ptr(err_flag), _stream(stream))
+        c, b, query.data_ptr(), *qs, heads, c.head_dim ** -0.5 if scale is None else float(scale), bool(causal), int(window),
+        out.data_ptr(), *os_, _ptr(lse), _ptr(workspace), nbytes, _ptr(err_flag), _stream(stream))
     _check("kvx_paged_attention", st)
 
 
@@ -784,20 +804,14 @@ def kvx_attention_mass(query, kv_cache, block_table, q_offsets, context_lens, ls
     """Add to mass (float32 [num_reqs][num_kv_heads][width]) the attention weight that the batch's
     queries give to every cached token, summed over the query heads of each KV head; lse is
     kvx_paged_attention's."""
-    import torch
-
     c = _cache(kv_cache, layout)
-    b = _batch(query, c, block_table, q_offsets, context_lens, max_query_len, max_context_len)
-    heads = query.shape[1]
-    _want(lse, torch.float32, "lse")
-    if lse.shape != query.shape[:2]:
-        raise ValueError("kvx: lse must be [num_tokens][heads]")
-    _want_lists(mass, "mass", b.num_reqs, c.num_kv_heads)
-    _on_current_device(query, getattr(c, "tensor", None), block_table, q_offsets, context_lens, lse, mass, err_flag)
+    b, heads, qs = _batch(query, c, block_table, q_offsets, context_lens, max_query_len, max_context_len)
+    _want_lse(lse, b.num_tokens, heads)
+    m = _lists(mass, "mass", b.num_reqs, c.num_kv_heads)
+    _on_current_device((query, c.tensor, block_table, q_offsets, context_lens, lse, mass, err_flag))
     st = _F["kvx_attention_mass"](
-        ctypes.byref(c), ctypes.byref(b), _ptr(query), _step(query, 0) * 2, _step(query, 1) * 2, heads,
-        c.head_dim ** -0.5 if scale is None else float(scale), int(causal), int(window), _ptr(lse), _ptr(mass),
-        _step(mass, 0), _step(mass, 1), mass.shape[2], _ptr(err_flag), _stream(stream))
+        c, b, query.data_ptr(), *qs, heads, c.head_dim ** -0.5 if scale is None else float(scale), bool(causal), int(window),
+        lse.data_ptr(), mass.data_ptr(), *m, _ptr(err_flag), _stream(stream))
     _check("kvx_attention_mass", st)
 
 
@@ -811,13 +825,13 @@ def kvx_evict_select(mass, context_lens, budget: int, sink: int, recent: int, ke
     _want(keep, torch.int32, "keep")
     _want(new_lens, torch.int64, "new_lens")
     R = context_lens.numel()
-    _want_lists(mass, "mass", R, None)
-    if keep.shape != (R, mass.shape[1], int(budget)) or new_lens.numel() != R:
+    m = _lists(mass, "mass", R, None)
+    heads = mass.shape[1]
+    if tuple(keep.shape) != (R, heads, int(budget)) or new_lens.numel() != R:
         raise ValueError("kvx: keep must be [num_reqs][heads][budget] and new_lens [num_reqs]")
-    _on_current_device(mass, context_lens, keep, new_lens, err_flag)
-    st = _F["kvx_evict_select"](_ptr(mass), _step(mass, 0), _step(mass, 1), mass.shape[2], R, mass.shape[1],
-                                _ptr(context_lens), int(budget), int(sink), int(recent), _ptr(keep), _ptr(new_lens),
-                                _ptr(err_flag), _stream(stream))
+    _on_current_device((mass, context_lens, keep, new_lens, err_flag))
+    st = _F["kvx_evict_select"](mass.data_ptr(), *m, R, heads, context_lens.data_ptr(), int(budget), int(sink), int(recent),
+                                keep.data_ptr(), new_lens.data_ptr(), _ptr(err_flag), _stream(stream))
     _check("kvx_evict_select", st)
 
 
@@ -828,24 +842,21 @@ def kvx_evict_compact(kv_cache, block_table, dst_block_table, keep, mass=None, m
     import torch
 
     c = _cache(kv_cache, layout)
-    _want_table(block_table)
-    _want_table(dst_block_table, "dst_block_table")
     _want(keep, torch.int32, "keep")
-    R = block_table.shape[0]
-    if keep.dim() != 3 or keep.shape[0] != R or dst_block_table.shape[0] != R:
-        raise ValueError("kvx: keep must be [num_reqs][heads][budget], with a row of both tables a request")
-    if keep.shape[1] == 0 or c.num_kv_heads % keep.shape[1]:
+    shape = keep.shape
+    if len(shape) != 3:
+        raise ValueError("kvx: keep must be [num_reqs][heads][budget]")
+    R, heads, budget = shape
+    src, dst = _table(block_table, R), _table(dst_block_table, R, "dst_block_table")
+    if heads == 0 or c.num_kv_heads % heads:
         raise ValueError("kvx: the KV heads must be a multiple of the heads that chose")
     if (mass is None) != (mass_out is None):
         raise ValueError("kvx: mass and mass_out go together")
-    m = (0, 0, 0, 0, 0, 0)
+    m, mo, m_ptr, mo_ptr = (0, 0, 0), (0, 0, 0), None, None
     if mass is not None:
-        _want_lists(mass, "mass", R, keep.shape[1])
-        _want_lists(mass_out, "mass_out", R, keep.shape[1])
-        m = (_step(mass, 0), _step(mass, 1), mass.shape[2], _step(mass_out, 0), _step(mass_out, 1), mass_out.shape[2])
-    _on_current_device(getattr(c, "tensor", None), block_table, dst_block_table, keep, mass, mass_out, err_flag)
-    st = _F["kvx_evict_compact"](
-        ctypes.byref(c), _ptr(block_table), block_table.shape[1], _row_stride(block_table), _ptr(dst_block_table),
-        dst_block_table.shape[1], _row_stride(dst_block_table), R, keep.shape[1], _ptr(keep), keep.shape[2],
-        _ptr(mass), m[0], m[1], m[2], _ptr(mass_out), m[3], m[4], m[5], _ptr(err_flag), _stream(stream))
+        m, mo = _lists(mass, "mass", R, heads), _lists(mass_out, "mass_out", R, heads)
+        m_ptr, mo_ptr = mass.data_ptr(), mass_out.data_ptr()
+    _on_current_device((c.tensor, block_table, dst_block_table, keep, mass, mass_out, err_flag))
+    st = _F["kvx_evict_compact"](c, block_table.data_ptr(), *src, dst_block_table.data_ptr(), *dst, R, heads,
+                                 keep.data_ptr(), budget, m_ptr, *m, mo_ptr, *mo, _ptr(err_flag), _stream(stream))
     _check("kvx_evict_compact", st)
