@@ -22,13 +22,19 @@ __device__ __forceinline__ uint32_t rank_of(float m) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One workgroup a list. The rank of the last kept slot is found digit by digit from the top (a
-// histogram of 8 bits a round over the slots that agree with the digits found); then one ordered
-// pass writes the slots above it and the lowest ones that equal it.
+// One workgroup a list. The masses are read once, into registers (lists beyond kSelSlots in pieces, again for every
+// digit). The rank of the last kept slot is found digit by digit from the top: a histogram of 8
+// bits a round over the slots that agree with the digits found. Then the slots above it and the lowest ones that
+// equal it are written in order, their places from counts by wavefront and 64 slots. What bounds it
+// is the chain of rounds, each a pass through LDS (8 x 8 lists of 9216: 24 -> 15 us with the registers).
+constexpr int kSelRegs = 16;
+constexpr int kSelSlots = kSelRegs * kSelThreads;
+constexpr int kSelCopies = 4;  // histograms, by wavefront: equal digits of different wavefronts do not collide
+
 __global__ __launch_bounds__(kSelThreads) void select_kernel(SelectArgs a) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t waves_gt[kSelWaves], waves_eq[kSelWaves];
-  __shared__ uint32_t found[2];  // digit, slots still wanted among those that have it
+  __shared__ uint32_t hist[kSelCopies][256];
+  __shared__ uint32_t counts[2][kSelRegs * kSelWaves];  // above the rank, equal to it: of 64 slots each, in order
+  __shared__ uint32_t found[4];  // digit, slots still wanted among those that have it; totals of a piece
   const int r = blockIdx.x / a.num_heads, h = blockIdx.x - r * a.num_heads;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t c = a.context_lens[r];
@@ -43,21 +49,42 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(SelectArgs a) {
   }
   const float* mass = a.mass + r * a.req_stride + h * a.head_stride;
   const int last = n - a.recent;
-  auto rank_at = [&](int j) -> uint32_t {
-    return j < a.sink || j >= last ? 0xffffffffu : rank_of(mass[j]);
+  uint32_t k[kSelRegs];
+  auto load = [&](int64_t j0) {
+    float m[kSelRegs];
+#pragma unroll
+    for (int i = 0; i < kSelRegs; ++i) {
+      const int64_t j = j0 + i * kSelThreads + tid;
+      if (j - tid < n) m[i] = gload<float>(mass + (j < n ? j : 0));
+    }
+#pragma unroll
+    for (int i = 0; i < kSelRegs; ++i) {
+      const int64_t j = j0 + i * kSelThreads + tid;
+      if (j - tid < n) k[i] = j < a.sink || j >= last ? 0xffffffffu : rank_of(m[i]);
+    }
   };
+  load(0);
   uint32_t prefix = 0, mask = 0, want = (uint32_t)want_all;
   for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
+    (&hist[0][0])[tid] = 0;
     __syncthreads();
-    for (int j = tid; j < n; j += kSelThreads) {
-      const uint32_t k = rank_at(j);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1u);
+    for (int64_t j0 = 0; j0 < n; j0 += kSelSlots) {
+      if (n > kSelSlots) load(j0);
+#pragma unroll
+      for (int i = 0; i < kSelRegs; ++i) {
+        const int64_t j = j0 + i * kSelThreads + tid;
+        if (j - tid >= n) break;
+        if (j < n && (k[i] & mask) == prefix) atomicAdd(&hist[wave % kSelCopies][(k[i] >> shift) & 255], 1u);
+      }
     }
     __syncthreads();
     if (wave == 0) {  // lane l: bins 255-4l .. 252-4l, from the largest down
       uint32_t b[4], sum = 0;
-      for (int i = 0; i < 4; ++i) sum += b[i] = hist[255 - 4 * lane - i];
+      for (int i = 0; i < 4; ++i) {
+        b[i] = 0;
+        for (int v = 0; v < kSelCopies; ++v) b[i] += hist[v][255 - 4 * lane - i];
+        sum += b[i];
+      }
       uint32_t upto = sum;
       for (int d = 1; d < 64; d <<= 1) {
         const uint32_t o = __shfl_up(upto, d);
@@ -76,41 +103,68 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(SelectArgs a) {
     prefix |= found[0] << shift;
     mask |= 255u << shift;
     want = found[1];
-    __syncthreads();
   }
   uint32_t base = 0, ties = want;  // slots written so far; equal slots still to write
-  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const uint32_t k = j < n ? rank_at(j) : 0;
-    const bool gt = j < n && k > prefix, eq = j < n && k == prefix;
-    const uint64_t bg = __ballot(gt), be = __ballot(eq), under = (1ull << lane) - 1;
-    if (lane == 0) {
-      waves_gt[wave] = __popcll(bg);
-      waves_eq[wave] = __popcll(be);
+  for (int64_t j0 = 0; j0 < n; j0 += kSelSlots) {
+    if (n > kSelSlots) load(j0);
+    uint64_t gt[kSelRegs], eq[kSelRegs];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSelRegs; ++i) {
+      const int64_t j = j0 + i * kSelThreads + tid;
+      if (j - tid >= n) {  // this row of 1024 slots and the ones after it are behind the list
+        gt[i] = eq[i] = 0;
+        if (lane < 2) counts[lane][i * kSelWaves + wave] = 0;
+        continue;
+      }
+      gt[i] = __ballot(j < n && k[i] > prefix);
+      eq[i] = __ballot(j < n && k[i] == prefix);
+      if (lane == 0) {
+        counts[0][i * kSelWaves + wave] = __popcll(gt[i]);
+        counts[1][i * kSelWaves + wave] = __popcll(eq[i]);
+      }
     }
     __syncthreads();
-    uint32_t g = 0, e = 0, all_g = 0, all_e = 0;
-    for (int w = 0; w < kSelWaves; ++w) {
-      if (w < wave) g += waves_gt[w], e += waves_eq[w];
-      all_g += waves_gt[w], all_e += waves_eq[w];
+    if (wave < 2) {  // each count becomes the sum of those before it: lane l's are 4l .. 4l+3
+      uint32_t* const at = counts[wave] + 4 * lane;
+      uint32_t v[4], sum = 0;
+      for (int i = 0; i < 4; ++i) {
+        v[i] = sum;
+        sum += at[i];
+      }
+      uint32_t upto = sum;
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = __shfl_up(upto, d);
+        if (lane >= d) upto += o;
+      }
+      for (int i = 0; i < 4; ++i) at[i] = v[i] + upto - sum;
+      if (lane == 63) found[2 + wave] = upto;
     }
-    g += __popcll(bg & under);
-    e += __popcll(be & under);
-    const uint32_t e_kept = e < ties ? e : ties;
-    if (gt || (eq && e < ties)) keep[base + g + e_kept] = j;
-    const uint32_t t = all_e < ties ? all_e : ties;
-    base += all_g + t;
-    ties -= t;
     __syncthreads();
+    const uint64_t under = (1ull << lane) - 1;
+#pragma unroll
+    for (int i = 0; i < kSelRegs; ++i) {
+      if (j0 + i * kSelThreads >= n) break;
+      const uint32_t g = counts[0][i * kSelWaves + wave] + __popcll(gt[i] & under);
+      const uint32_t e = counts[1][i * kSelWaves + wave] + __popcll(eq[i] & under);
+      if (((gt[i] >> lane) & 1) || (((eq[i] >> lane) & 1) && e < ties))
+        keep[base + g + (e < ties ? e : ties)] = (int32_t)(j0 + i * kSelThreads + tid);
+    }
+    const uint32_t e_kept = found[3] < ties ? found[3] : ties;
+    base += found[2] + e_kept;
+    ties -= e_kept;
   }
 }
+static_assert(kSelRegs * kSelWaves == 256 && kSelCopies * 256 == kSelThreads, "one entry a thread or four a lane");
 
 // --------------------------------------------------------------------------------------
 // moving
 // --------------------------------------------------------------------------------------
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 8;
+// Rows in flight a thread, moved past the caches like the copies of whole blocks: 4 against 8 (a batch's eviction 75 against
+// 78 us), and 73 with non-temporal loads and stores.
+constexpr int kMoveUnroll = 4;
 
 // Every load of the workgroup has its value before any wavefront goes on to store.
 __device__ __forceinline__ void loads_landed() {
@@ -201,16 +255,17 @@ __global__ __launch_bounds__(kMoveThreads) void compact_kernel(CompactArgs a, Bl
         move[u] = move[u] && !(piece[u] >> 16);
         const char* src = (const char*)cache.base + at + (piece[u] & 0xffff);
         if (move[u]) src += sb[u] * cache.block_stride_bytes + (int64_t)k[u] * cache.token_stride_bytes;
-        v[u] = gload<u32x4>(src);
+        v[u] = __builtin_nontemporal_load((const __attribute__((address_space(1))) u32x4*)src);
       }
       loads_landed();
 #pragma unroll
       for (int u = 0; u < kMoveUnroll; ++u) {
         const int32_t i = (int32_t)(t0 + row[u]);
         if (move[u])
-          gstore((char*)cache.base + db[u] * cache.block_stride_bytes +
-                     (int64_t)(i - block_of(div, i) * div.size) * cache.token_stride_bytes + at + (piece[u] & 0xffff),
-                 v[u]);
+          __builtin_nontemporal_store(
+              v[u], (__attribute__((address_space(1))) u32x4*)(
+                        (char*)cache.base + db[u] * cache.block_stride_bytes +
+                        (int64_t)(i - block_of(div, i) * div.size) * cache.token_stride_bytes + at + (piece[u] & 0xffff)));
       }
     }
   }
