@@ -290,7 +290,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   constexpr int VPR = DP / 8, RPI = 64 / VPR, NI = KW / RPI;
   constexpr int KT = KEYS ? 1 : 2, KSTEPS = DP / 16, DT = DP / 32;
   constexpr int KROW = DP * 2 + 16, VROW = DP * 2 + 64;  // bytes of a row in LDS
-  __shared__ __align__(16) char smem[BN * (KROW + VROW) + BN];
+  // Q in registers, but for the widest heads' few rows in LDS: their tiles and sums take the registers
+  constexpr bool Q_LDS = KEYS && DP > 128;
+  __shared__ __align__(16) char smem[BN * (KROW + VROW) + BN + (Q_LDS ? 32 * KROW : 0)];
   char* const sk = smem;
   char* const sv = smem + BN * KROW;
   uint8_t* const flags = (uint8_t*)(smem + BN * (KROW + VROW));
@@ -340,7 +342,11 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
     x.tile = (int32_t)quotient(begin - q.step0, steps);
     from = (int32_t)(begin - q.step0 - (int64_t)x.tile * steps);
   } else {
-    x = find_rows<ROWS>(a, sp.tiles - 1 - index, group, cap, lane);
+    // The longest tiles first; every other round of 256 workgroups (one a CU) the other way round, so
+    // that a CU's second tile makes up for its first.
+    const int per = 256 / a.cache.num_kv_heads > 0 ? 256 / a.cache.num_kv_heads : 1, round = index / per;
+    const int back = (round + 1) * per < sp.tiles ? (round + 1) * per : sp.tiles;
+    x = find_rows<ROWS>(a, sp.tiles - 1 - (round & 1 ? back - 1 - (index - round * per) : index), group, cap, lane);
     if ((int64_t)x.tile * ROWS >= (int64_t)x.tokens * group) return;
   }
   int errs = 0;
@@ -374,14 +380,18 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   }
 
   // Q: lane n's row, eight elements a step
-  u32x4 q[KSTEPS];
+  u32x4 q[Q_LDS ? 1 : KSTEPS];
+  char* const sq = smem + BN * (KROW + VROW) + BN + n * KROW + hf * 16;
   {
     const char* p = a.query.base + q_row * a.query.token_stride + head * a.query.head_stride;
 #pragma unroll
     for (int s = 0; s < KSTEPS; ++s) {
-      q[s] = u32x4{0, 0, 0, 0};
-      if (used && 2 * s + hf < vecs) q[s] = gload<u32x4>(p + (2 * s + hf) * 16);
+      u32x4 v = {0, 0, 0, 0};
+      if (used && 2 * s + hf < vecs) v = gload<u32x4>(p + (2 * s + hf) * 16);
+      if constexpr (!Q_LDS) q[s] = v;
+      else if (s % 4 == w) *(u32x4*)(sq + s * 32) = v;  // a quarter of the steps each
     }
+    if constexpr (Q_LDS) __syncthreads();
   }
 
   const char* const kbase = (const char*)a.cache.base + g * a.cache.head_stride_bytes + (c < vecs ? c : 0) * 16;
@@ -461,7 +471,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   }
   // Q is here before the loop: a wait for it inside would be one for the loads in flight as well
 #pragma unroll
-  for (int st = 0; st < KSTEPS; ++st) asm volatile("" : "+v"(q[st]));
+  for (int st = 0; st < (Q_LDS ? 0 : KSTEPS); ++st) asm volatile("" : "+v"(q[st]));
   for (int t = tb; t < te; ++t) {
     const int k0 = t * BN;
     // every row sees every slot of an inner tile
@@ -510,9 +520,11 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
       s[kt] = f32x16{};
 #pragma unroll
       for (int st = 0; st < KSTEPS; ++st)
-        s[kt] = mfma(E(), *(const u32x4*)(sk_get + kt * 32 * KROW + st * 32), q[st], s[kt]);
+        s[kt] = mfma(E(), *(const u32x4*)(sk_get + kt * 32 * KROW + st * 32),
+                     Q_LDS ? *(const u32x4*)(sq + st * 32) : q[Q_LDS ? 0 : st], s[kt]);
     }
     // K is read eight pieces ahead of the products: read as they are needed, each would wait for LDS
+    if constexpr (!Q_LDS) {
     __builtin_amdgcn_sched_group_barrier(kDsRead, 8, 0);
 #pragma unroll
     for (int i = 0; i < KT * KSTEPS - 8; ++i) {
@@ -520,6 +532,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
       __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
     }
     __builtin_amdgcn_sched_group_barrier(kMfma, 8, 0);
+    }
     if (!inner || ~there) {
       const int at = here(k0 + kw + 4 * hf), lo = see.x - at, hi = see.y - at;
 #pragma unroll
@@ -822,9 +835,10 @@ Plan plan_attention(const kvx_paged_cache& c, const kvx_batch& b, int32_t num_he
   if (busy > p.tiles) busy = p.tiles;
   if (busy < 1) busy = 1;
   const int64_t context = b.max_context_len < kMaxContext ? b.max_context_len : kMaxContext;
-  int64_t shares = kFill / c.num_kv_heads, most = busy * (context / slots) / kMinSteps;
+  const int fill = c.head_dim > 128 ? kFill / 2 : kFill;  // the widest heads' tiles leave room for one workgroup a CU
+  int64_t shares = fill / c.num_kv_heads, most = busy * (context / slots) / kMinSteps;
   if (shares > most) shares = most;
-  const bool uneven = busy * c.num_kv_heads < (p.keys ? 4 * kFill : kFill);
+  const bool uneven = busy * c.num_kv_heads < (p.keys ? 4 * fill : fill);
   p.shares = uneven && shares > (p.keys ? busy / 4 : busy) ? (int32_t)shares : 0;
   return p;
 }
@@ -911,6 +925,53 @@ struct RowTile {
       *(u32x4*)(lds + (i * RPI + lane / VPR) * ROW + c * 16) = VPR == vecs || c < vecs ? v[i] : u32x4{0, 0, 0, 0};
   }
 };
+
+// Adds the weights exp(x - lse) of 64 slots from k0 to a lane's sums: its row sees slots [now.x, now.y).
+struct Nothing {
+  __device__ __forceinline__ void operator()() const {}
+};
+template <class F = Nothing>  // order: of the weights and what stands before them
+__device__ __forceinline__ void add_weights(f32x16 (&s)[2], f32x16 (&sum)[2], int2 now, int k0, int hf, float c1, float ref,
+                                            F order = F()) {
+  const bool whole = __all(now.x <= k0 && now.y >= k0 + 64);
+#pragma unroll
+  for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[kt][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][i], c1, -ref));
+#pragma unroll
+  for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+v"(s[kt][i]));  // all formed here, not behind the branch
+  order();
+#pragma unroll
+  for (int kt = 0; kt < 2; ++kt) {
+    if (!whole) {
+      const int to = here(k0 + kt * 32 + 4 * hf), lo = now.x - to, hi = now.y - to;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int o = 8 * (i / 4) + i % 4;
+        if (o < lo || o >= hi) s[kt][i] = 0;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum[kt][i] += s[kt][i];
+  }
+}
+// The lanes' sums of 64 slots joined through LDS of the wavefront's own: lane l gets slot l's.
+template <int LROW>
+__device__ __forceinline__ float row_sums(char* own, const f32x16 (&sum)[2], int lane) {
+  float* const mine = (float*)own;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mine[(kt * 32 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4) * LROW + (lane & 31)] = sum[kt][i];
+  __builtin_amdgcn_wave_barrier();
+  f32x4 t = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t += *(const f32x4*)(mine + lane * LROW + i * 4);
+  return (t[0] + t[1]) + (t[2] + t[3]);
+}
 
 // A wavefront owns 64 slots of one KV head: their K stays in registers, the query rows pass by 32 at a
 // time (through LDS, for all four wavefronts), and the weights exp(x - lse) of S^T = K Q^T add up in the
@@ -999,54 +1060,174 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void mass_kernel(MassArgs m
       lse = gload<float>(a.lse + (x.q0 + token) * a.num_heads + head);
       see = row0 + n < row_to ? sees(a, x, token) : int2{0, 0};
     };
-    if (row_from < row_to) load_rows(row_from);
-    int turn = 0;
-    for (int row0 = row_from; row0 < row_to; row0 += 32, turn ^= 1) {
+    // The products of one tile of rows run while the weights of the one before are formed.
+    f32x16 s[2][2];
+    int2 now[2];
+    float ref[2];
+    int row0 = row_from, turn = 0;
+    auto scores = [&](int to) {
       char* const tile = qs + turn * 32 * ROW;
       q.put(tile + w * 8 * ROW, lane, vecs);
-      const float ref = lse * kLog2e;
-      const int2 now = lse == -INFINITY ? int2{0, 0} : see;
+      ref[to] = lse * kLog2e;
+      now[to] = lse == -INFINITY ? int2{0, 0} : see;
       // The other tile is written next, which every wavefront has read before this barrier.
       lds_barrier();
-      if (row0 + 32 < row_to) load_rows(row0 + 32);
-      if (!__any(now.y > k0 && now.x < k0 + 64)) continue;
-      f32x16 s[2] = {f32x16{}, f32x16{}};
+      row0 += 32;
+      turn ^= 1;
+      if (row0 < row_to) load_rows(row0);
+      s[to][0] = s[to][1] = f32x16{};
 #pragma unroll
       for (int st = 0; st < KSTEPS; ++st) {
         const u32x4 qf = *(const u32x4*)(tile + n * ROW + st * 32 + hf * 16);
-        s[0] = mfma(E(), k[0][st], qf, s[0]);
-        s[1] = mfma(E(), k[1][st], qf, s[1]);
+        s[to][0] = mfma(E(), k[0][st], qf, s[to][0]);
+        s[to][1] = mfma(E(), k[1][st], qf, s[to][1]);
       }
-      const bool whole = __all(now.x <= k0 && now.y >= k0 + 64);
+    };
+    auto interleave = [&]() {
+      __builtin_amdgcn_sched_group_barrier(kDsRead, 2, 2);
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[kt][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][i], c1, -ref));
-        if (!whole) {
-          const int to = here(k0 + kt * 32 + 4 * hf), lo = now.x - to, hi = now.y - to;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int o = 8 * (i / 4) + i % 4;
-            if (o < lo || o >= hi) s[kt][i] = 0;
-          }
+      for (int st = 0; st < KSTEPS; ++st) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 2);
+        __builtin_amdgcn_sched_group_barrier(kVector, 64 / (2 * KSTEPS), 2);
+        __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 2);
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 2);
+        __builtin_amdgcn_sched_group_barrier(kVector, 64 / (2 * KSTEPS), 2);
+      }
+    };
+    if (row0 < row_to) {
+      load_rows(row0);
+      scores(0);
+      for (;;) {
+        if (row0 >= row_to) {
+          add_weights(s[0], sum, now[0], k0, hf, c1, ref[0]);
+          break;
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum[kt][i] += s[kt][i];
+        scores(1);
+        add_weights(s[0], sum, now[0], k0, hf, c1, ref[0], interleave);
+        if (row0 >= row_to) {
+          add_weights(s[1], sum, now[1], k0, hf, c1, ref[1]);
+          break;
+        }
+        scores(0);
+        add_weights(s[1], sum, now[1], k0, hf, c1, ref[1], interleave);
       }
     }
-    float* const mine = (float*)own;
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) mine[(kt * 32 + 8 * (i / 4) + 4 * hf + i % 4) * LROW + n] = sum[kt][i];
-    __builtin_amdgcn_wave_barrier();
-    f32x4 t = {};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t += *(const f32x4*)(mine + lane * LROW + i * 4);
-    if (ok) gstore(mass, before + ((t[0] + t[1]) + (t[2] + t[3])));
+    const float total = row_sums<LROW>(own, sum, lane);
+    if (ok) gstore(mass, before + total);
     lds_barrier();  // the query tiles and the partial sums are free again
   }
   if (errs) raise(a.err, errs);
+}
+
+// The same where there are too few slots to fill the GPU that way, as with a whole prompt's rows: a workgroup's eight
+// wavefronts share 64 slots and take the tiles of rows in turn, each through LDS of its own; their sums
+// meet at the end, in order (a prompt of 8192 tokens of 8 heads on one KV head: 2084 -> 547 us).
+constexpr int kMassWaves = 8;
+
+template <class E, int DP>
+__global__ __launch_bounds__(64 * kMassWaves, DP <= 128 ? 2 : 1) void mass_rows_kernel(MassArgs ma, BlockDiv div) {
+  typedef RowTile<DP, 64 / kMassWaves> KTile;  // a wavefront's share of 64 slots
+  typedef RowTile<DP, 32> QTile;
+  constexpr int KSTEPS = DP / 16, LROW = 36, ROW = QTile::ROW;
+  constexpr int OWN = 32 * ROW > 64 * LROW * 4 ? 32 * ROW : 64 * LROW * 4;
+  __shared__ __align__(16) char smem[kMassWaves * OWN];
+  __shared__ float sums[kMassWaves][64];
+  const AttendArgs& a = ma.at;
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform((int32_t)(tid >> 6));
+  const int n = lane & 31, hf = lane >> 5, g = blockIdx.x, r = blockIdx.z;
+  const int group = a.num_heads / a.cache.num_kv_heads, vecs = a.cache.head_dim / 8;
+  const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size;
+  if (blockIdx.y == 0 && g == 0 && r == 0) check_batch(a, cap, tid, 64 * kMassWaves);
+  MassRows m;
+  if (!mass_rows(ma, r, group, cap, &m)) return;
+  const Rows& x = m.x;
+  const float c1 = a.scale * kLog2e;
+  const int32_t* const table = a.batch.block_table + r * a.batch.bt_row_stride;
+  char* const own = smem + w * OWN;
+  int errs = 0;
+
+  for (int64_t at = (int64_t)blockIdx.y * 64; at < m.end; at += (int64_t)gridDim.y * 64) {
+    if (at + 64 <= m.from) continue;
+    const int k0 = (int)at, j = k0 + lane;
+    const bool in = j >= m.from && j < m.end;
+    const int32_t id = in ? table[block_of(div, j)] : -1;
+    const bool ok = in && (uint32_t)id < (uint64_t)a.cache.num_blocks;
+    if (in && !ok) errs |= KVX_DEVERR_BLOCK_RANGE;
+    const int64_t off = ok ? id * a.cache.block_stride_bytes +
+                                 (int64_t)(j - block_of(div, j) * div.size) * a.cache.token_stride_bytes
+                           : 0;
+    u32x4 k[2][KSTEPS];
+    {
+      KTile t;
+      const char* const base = (const char*)a.cache.base + g * a.cache.head_stride_bytes;
+      constexpr int SHARE = 64 / kMassWaves;
+      t.load([&](int i) { return base + __shfl(off, w * SHARE + i * KTile::RPI + lane / KTile::VPR); }, lane, vecs);
+      t.put(smem + w * SHARE * ROW, lane, vecs);
+      lds_barrier();
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int st = 0; st < KSTEPS; ++st)
+          k[kt][st] = *(const u32x4*)(smem + (kt * 32 + n) * ROW + st * 32 + hf * 16);
+      lds_barrier();
+    }
+    int row_from = 0, row_to = m.rows;
+    if (a.causal) {
+      const int64_t t0 = at - x.context + x.tokens, t1 = t0 + 64 + a.window;
+      if (t0 > 0) row_from = t0 < x.tokens ? (int)t0 * group : m.rows;
+      if (t1 < x.tokens) row_to = t1 > 0 ? (int)t1 * group : 0;
+    }
+    f32x16 sum[2] = {f32x16{}, f32x16{}};
+    QTile q;
+    int2 see;
+    float lse;
+    auto row_of = [&](int row, int* token, int* head) {  // a row past the last reads the first token's
+      *token = row < row_to ? row / group : 0;
+      *head = g * group + (row < row_to ? row - *token * group : 0);
+    };
+    auto load_rows = [&](int row0) {
+      q.load([&](int i) {
+        int token, head;
+        row_of(row0 + i * QTile::RPI + lane / QTile::VPR, &token, &head);
+        return a.query.base + (x.q0 + token) * a.query.token_stride + head * a.query.head_stride;
+      }, lane, vecs);
+      int token, head;
+      row_of(row0 + n, &token, &head);
+      lse = gload<float>(a.lse + (x.q0 + token) * a.num_heads + head);
+      see = row0 + n < row_to ? sees(a, x, token) : int2{0, 0};
+    };
+    constexpr int STEP = 32 * kMassWaves;
+    int row0 = row_from + w * 32;
+    if (row0 < row_to) load_rows(row0);
+    for (; row0 < row_to; row0 += STEP) {
+      q.put(own, lane, vecs);
+      const float ref = lse * kLog2e;
+      const int2 now = lse == -INFINITY ? int2{0, 0} : see;
+      __builtin_amdgcn_wave_barrier();
+      if (row0 < row_to - STEP) load_rows(row0 + STEP);
+      f32x16 s[2] = {f32x16{}, f32x16{}};
+#pragma unroll
+      for (int st = 0; st < KSTEPS; ++st) {
+        const u32x4 qf = *(const u32x4*)(own + n * ROW + st * 32 + hf * 16);
+        s[0] = mfma(E(), k[0][st], qf, s[0]);
+        s[1] = mfma(E(), k[1][st], qf, s[1]);
+      }
+      __builtin_amdgcn_wave_barrier();
+      add_weights(s, sum, now, k0, hf, c1, ref);
+    }
+    const float total = row_sums<LROW>(own, sum, lane);
+    sums[w][lane] = total;
+    lds_barrier();
+    if (w == 0 && ok) {
+      float* const mass = ma.mass + r * ma.mass_req_stride + g * ma.mass_head_stride + j;
+      float t = 0;
+#pragma unroll
+      for (int i = 0; i < kMassWaves; ++i) t += sums[i][lane];
+      gstore(mass, gload<float>(mass) + t);
+    }
+    lds_barrier();
+  }
+  if (errs && w == 0) raise(a.err, errs);
 }
 
 // The same for up to 32 query rows of a KV head, a decode step's: the rows stay in registers and the
@@ -1169,18 +1350,21 @@ __global__ __launch_bounds__(256, DP <= 128 ? 3 : 2) void mass_few_kernel(MassAr
   if (errs) raise(a.err, errs);
 }
 
+enum { kMassBySlots, kMassByRows, kMassFew };
+
+template <class E, int DP>
+void launch_mass_dim(const MassArgs& m, BlockDiv div, dim3 grid, int how, int span, hipStream_t stream) {
+  if (how == kMassFew) mass_few_kernel<E, DP><<<grid, 256, 0, stream>>>(m, div, span);
+  else if (how == kMassByRows) mass_rows_kernel<E, DP><<<grid, 64 * kMassWaves, 0, stream>>>(m, div);
+  else mass_kernel<E, DP><<<grid, 256, 0, stream>>>(m, div);
+}
+
 template <class E>
-void launch_mass_dims(const MassArgs& m, BlockDiv div, dim3 grid, int span, hipStream_t stream) {
+void launch_mass_dims(const MassArgs& m, BlockDiv div, dim3 grid, int how, int span, hipStream_t stream) {
   const int dim = m.at.cache.head_dim;
-  if (span) {
-    if (dim <= 64) mass_few_kernel<E, 64><<<grid, 256, 0, stream>>>(m, div, span);
-    else if (dim <= 128) mass_few_kernel<E, 128><<<grid, 256, 0, stream>>>(m, div, span);
-    else mass_few_kernel<E, 256><<<grid, 256, 0, stream>>>(m, div, span);
-  } else {
-    if (dim <= 64) mass_kernel<E, 64><<<grid, 256, 0, stream>>>(m, div);
-    else if (dim <= 128) mass_kernel<E, 128><<<grid, 256, 0, stream>>>(m, div);
-    else mass_kernel<E, 256><<<grid, 256, 0, stream>>>(m, div);
-  }
+  if (dim <= 64) launch_mass_dim<E, 64>(m, div, grid, how, span, stream);
+  else if (dim <= 128) launch_mass_dim<E, 128>(m, div, grid, how, span, stream);
+  else launch_mass_dim<E, 256>(m, div, grid, how, span, stream);
 }
 
 }  // namespace
@@ -1214,20 +1398,25 @@ hipError_t launch_mass(const MassArgs& m, hipStream_t stream) {
   if (slots > b.max_context_len) slots = b.max_context_len > 0 ? b.max_context_len : 1;
   const int64_t longest = b.max_query_len < b.num_tokens ? b.max_query_len : b.num_tokens;
   const int64_t lists = (int64_t)b.num_reqs * m.at.cache.num_kv_heads;
+  // slots of a workgroup
   int64_t per = kMassSlots;
-  int span = 0;
+  int how = kMassBySlots;
   if (longest * (m.at.num_heads / m.at.cache.num_kv_heads) <= 32) {
-    // slots of a workgroup: a whole number of steps of its four wavefronts, few enough to fill the GPU
+    // a whole number of steps of its four wavefronts, few enough to fill the GPU
+    how = kMassFew;
     per = (slots * lists / kMassFill + 127) / 128 * 128;
     if (per < 128) per = 128;
     if (per > 4096) per = 4096;
-    span = (int)per;
+  } else if ((slots + kMassSlots - 1) / kMassSlots * lists < (m.at.cache.head_dim <= 128 ? kFill : kFill / 3)) {
+    how = kMassByRows;
+    per = 64;
   }
+  const int span = (int)per;
   const int64_t pieces = (slots + per - 1) / per;
   const dim3 grid(m.at.cache.num_kv_heads, (unsigned)(pieces < 65535 ? pieces : 65535), b.num_reqs);
   const BlockDiv div = block_div(m.at.cache.block_size);
-  if (m.at.cache.dtype == KVX_DTYPE_BF16) launch_mass_dims<Bf16>(m, div, grid, span, stream);
-  else launch_mass_dims<Fp16>(m, div, grid, span, stream);
+  if (m.at.cache.dtype == KVX_DTYPE_BF16) launch_mass_dims<Bf16>(m, div, grid, how, span, stream);
+  else launch_mass_dims<Fp16>(m, div, grid, how, span, stream);
   return hipGetLastError();
 }
 

@@ -163,6 +163,30 @@ def test_split_contexts(lens, heads):
     run(case, window=3000)
 
 
+def test_many_requests():
+    """More requests than a wavefront has lanes, empty ones among them: decode steps and chunks whose
+    work is shared out, and a single head whose tiles are not."""
+    rng = np.random.default_rng(12)
+    lens = [(int(n), int(c)) if n else (0, int(c)) for n, c in zip(rng.integers(0, 2, 150), rng.integers(1, 900, 150))]
+    run(A.Case(26, lens, heads=2, kv_heads=1, dim=64, extra=3))
+    lens = [(int(n), int(n + c)) for n, c in zip(rng.integers(0, 60, 90), rng.integers(0, 600, 90))]
+    run(A.Case(27, lens, heads=4, kv_heads=1, dim=64))
+    run(A.Case(28, lens, heads=4, kv_heads=1, dim=64), split=False, mass=False)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_masses_of_a_large_batch(dim):
+    """Enough slots to fill the GPU without splitting the rows: 5 heads a KV head, some windows."""
+    case = A.Case(29, [(8, 1100)] * 14 + [(9, 700), (7, 2000)], heads=40 if dim == 64 else 32, kv_heads=8, dim=dim)
+    run(case, window=0 if dim == 64 else 600)
+
+
+@pytest.mark.parametrize("dim,dtype", [(80, "bf16"), (256, "fp16")])
+def test_shared_work_of_other_dims(dim, dtype):
+    run(A.Case(30, [(1, 6000), (1, 200), (1, 3001)], heads=4, kv_heads=1, dim=dim, dtype=dtype))
+    run(A.Case(31, [(70, 3000), (3, 900)], heads=4, kv_heads=1, dim=dim, dtype=dtype, block=24))
+
+
 def test_every_workspace_size():
     """Any workspace from none to the full one is enough for right results."""
     K = kvx()
