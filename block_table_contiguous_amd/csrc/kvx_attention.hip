@@ -90,8 +90,8 @@ __device__ __forceinline__ Rows find_rows(const AttendArgs& a, int32_t tile, int
     const int i = lane * step < len ? lo + lane * step : lo;
     begin = clamp64(a.batch.q_offsets[i], 0, a.batch.num_tokens);
     const bool at = lane * step < len && begin * group / ROWS + i <= tile;
-    const int hit = __popcll(__ballot(at));
-    const int pick = hit ? hit - 1 : 0;
+    const uint64_t hit = __ballot(at);
+    const int pick = hit ? 63 - __builtin_clzll(hit) : 0;
     lo += pick * step;
     if (step == 1) break;
     len = len - pick * step < step ? len - pick * step : step;
@@ -347,13 +347,17 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
     const int per = 256 / a.cache.num_kv_heads > 0 ? 256 / a.cache.num_kv_heads : 1, round = index / per;
     const int back = (round + 1) * per < sp.tiles ? (round + 1) * per : sp.tiles;
     x = find_rows<ROWS>(a, sp.tiles - 1 - (round & 1 ? back - 1 - (index - round * per) : index), group, cap, lane);
-    if ((int64_t)x.tile * ROWS >= (int64_t)x.tokens * group) return;
+    // a spare tile, or offsets that are not a CSR
+    if (x.tile < 0 || (int64_t)x.tile * ROWS >= (int64_t)x.tokens * group) return;
   }
   int errs = 0;
   bool bad_blocks = false;
   for (;;) {
   const AttendArgs a = argument<AttendArgs>();
-  if constexpr (SHARED) to = from + left < steps ? (int)(from + left) : steps;
+  if constexpr (SHARED) {
+    if (tile0 + x.tile >= sp.tiles) break;  // offsets that are not a CSR: the workspace has no slots for more
+    to = from + left < steps ? (int)(from + left) : steps;
+  }
   const int row0 = x.tile * ROWS, rows = x.tokens * group;
 
   // this lane's row, what it sees, and what any row of the workgroup sees

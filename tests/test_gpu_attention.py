@@ -295,22 +295,31 @@ def test_bad_tables(n):
     run(case, err=K.DEVERR_TABLE_RANGE)
 
 
-@pytest.mark.parametrize("offsets", [[0, 50, 20, 60], [0, 10, 70, 1 << 40], [-3, 10, 20, 60]])
-def test_bad_offsets(offsets):
-    """Offsets that are not a CSR raise their bit and reach nothing outside the tensors."""
+@pytest.mark.parametrize("offsets", [[0, 50, 20, 60], [0, 10, 70, 1 << 40], [-3, 10, 20, 60], [55, 10, 20, 60], [60, 0, 60, 0],
+                                     [0, 60, 0, 60], [0, -5, 60, 61]])
+@pytest.mark.parametrize("split", [False, True])
+def test_bad_offsets(offsets, split):
+    """Offsets that are not a CSR raise their bit and reach nothing outside the tensors, among them
+    ones that give the same rows to several requests."""
     K = kvx()
-    case = A.Case(20, [(20, 60), (20, 60), (20, 60)], heads=4, kv_heads=2, dim=64)
-    q, cache, table, _, ctx = case.to()
-    off = torch.tensor(offsets, dtype=torch.int64, device=DEV)
-    guard = torch.full((62, 4, 64), 7.0, dtype=q.dtype, device=DEV)
-    err = torch.zeros(2, dtype=torch.int32, device=DEV)
-    lse = torch.zeros(60, 4, device=DEV)
-    K.kvx_paged_attention(q, cache, table, off, ctx, guard[1:61], lse, err_flag=err[:1])
-    m = torch.zeros(3, 2, 64, device=DEV)
-    K.kvx_attention_mass(q, cache, table, off, ctx, lse, m, err_flag=err[1:])
-    torch.cuda.synchronize()
-    assert err.tolist() == [K.DEVERR_OFFSETS] * 2
-    assert bool((guard[0] == 7).all()) and bool((guard[61] == 7).all())
+    for heads, ctx_len in ((4, 60), (64, 3000)):
+        case = A.Case(20, [(20, ctx_len), (20, 60), (20, ctx_len)], heads=heads, kv_heads=2, dim=64)
+        q, cache, table, _, ctx = case.to()
+        off = torch.tensor(offsets, dtype=torch.int64, device=DEV)
+        guard = torch.full((62, heads, 64), 7.0, dtype=q.dtype, device=DEV)
+        err = torch.zeros(2, dtype=torch.int32, device=DEV)
+        lses = torch.full((62, heads), 7.0, device=DEV)
+        n = K.attention_workspace_bytes(q, cache, 3, 20, ctx_len) if split else 0
+        ws = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+        K.kvx_paged_attention(q, cache, table, off, ctx, guard[1:61], lses[1:61], err_flag=err[:1], max_query_len=20,
+                              max_context_len=ctx_len, workspace=ws[:n] if n else None)
+        m = torch.zeros(3, 2, case.width * 16, device=DEV)
+        K.kvx_attention_mass(q, cache, table, off, ctx, torch.zeros(60, heads, device=DEV), m, err_flag=err[1:])
+        torch.cuda.synchronize()
+        assert err.tolist() == [K.DEVERR_OFFSETS] * 2
+        for t in (guard, lses):
+            assert bool((t[0] == 7).all()) and bool((t[61] == 7).all())
+        assert bool((ws[n:] == 0xA5).all()), "written past the workspace"
 
 
 def test_narrow_masses():
