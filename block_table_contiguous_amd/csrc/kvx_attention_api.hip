@@ -11,6 +11,7 @@
 namespace {
 
 constexpr int64_t kInt32Max = 0x7fffffff;
+constexpr int64_t kMaxGroups = (1 << 22) - 1;  // workgroups along a grid dimension, up to 1024 threads each
 
 inline kvx_status from_hip(hipError_t e) { return e == hipSuccess ? KVX_SUCCESS : KVX_ERR_HIP; }
 inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
@@ -53,7 +54,7 @@ kvx_status check_batch(const kvx_paged_cache* c, const kvx_batch* b, int32_t num
   if (!b || b->num_reqs < 0 || b->num_reqs > 65535 || b->num_tokens < 0 || b->max_query_len < 0 ||
       b->max_context_len < 0 || num_heads < 1 || num_heads % c->num_kv_heads != 0 ||
       !table_ok(b->num_reqs, b->max_blocks_per_req, b->bt_row_stride, c->block_size) ||
-      b->num_tokens > kInt32Max / num_heads || (int64_t)b->num_reqs * c->num_kv_heads > kInt32Max / 2)
+      b->num_tokens > kInt32Max / num_heads || (int64_t)b->num_reqs * c->num_kv_heads > kMaxGroups)
     return KVX_ERR_INVALID_ARGUMENT;
   return st;
 }
@@ -79,7 +80,7 @@ kvx_status kvx_rope_and_cache(const kvx_paged_cache* cache, const void* query,
                               int32_t* err_flag, hipStream_t stream) {
   kvx_status st = check_cache(cache);
   if (st == KVX_ERR_INVALID_ARGUMENT) return st;
-  if (num_tokens < 0 || num_tokens > kInt32Max || num_heads < 0 || num_heads > 65535 || num_axes < 1 ||
+  if (num_tokens < 0 || num_tokens > kMaxGroups || num_heads < 0 || num_heads > 65535 || num_axes < 1 ||
       num_axes > KVX_MAX_AXES || rot_dim < 16 || rot_dim > cache->head_dim || rot_dim % 16 != 0)
     return KVX_ERR_INVALID_ARGUMENT;
   const kvx_status rows[] = {
@@ -207,7 +208,7 @@ kvx_status kvx_evict_select(const float* mass, int64_t mass_req_stride, int64_t 
                             hipStream_t stream) {
   if (num_reqs < 0 || num_heads < 1 || mass_width < 0 || mass_width > kInt32Max || budget < 1 || budget > kInt32Max ||
       sink < 0 || recent < 0 || sink > budget || recent > budget - sink || !extent_ok(num_reqs, mass_req_stride) ||
-      !extent_ok(num_heads, mass_head_stride) || (int64_t)num_reqs * num_heads > kInt32Max)
+      !extent_ok(num_heads, mass_head_stride) || (int64_t)num_reqs * num_heads > kMaxGroups)
     return KVX_ERR_INVALID_ARGUMENT;
   if (num_reqs == 0) return KVX_SUCCESS;
   if ((!mass && mass_width > 0) || !context_lens || !keep || !new_lens || new_lens == context_lens)
@@ -233,7 +234,7 @@ kvx_status kvx_evict_compact(const kvx_paged_cache* cache, const int32_t* block_
       cache->num_blocks == 0 || max_blocks_per_req < 1 || dst_max_blocks_per_req < 1 ||
       !table_ok(num_reqs, max_blocks_per_req, bt_row_stride, cache->block_size) ||
       !table_ok(num_reqs, dst_max_blocks_per_req, dst_bt_row_stride, cache->block_size) ||
-      (int64_t)num_reqs * (2 * cache->num_kv_heads + num_heads) > kInt32Max || (mass == nullptr) != (mass_out == nullptr))
+      (int64_t)num_reqs * (2 * cache->num_kv_heads + num_heads) > kMaxGroups || (mass == nullptr) != (mass_out == nullptr))
     return KVX_ERR_INVALID_ARGUMENT;
   if (mass && (mass_width < 0 || mass_width > kInt32Max || mass_out_width < 0 || mass_out_width > kInt32Max ||
                !extent_ok(num_reqs, mass_req_stride) || !extent_ok(num_heads, mass_head_stride) ||

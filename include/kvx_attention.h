@@ -31,6 +31,10 @@ extern "C" {
 
 /* Largest head_dim; head_dim is a multiple of 8. */
 #define KVX_MAX_HEAD_DIM 256
+/* Requests times KV heads of a call (in kvx_evict_compact: times 2 KV heads + mass heads), and the tokens of
+ * kvx_rope_and_cache, are below 2^22; requests of kvx_paged_attention and kvx_attention_mass below
+ * 2^16. Larger ones return KVX_ERR_INVALID_ARGUMENT. */
+
 /* Most axes of a rotary position. */
 #define KVX_MAX_AXES 4
 

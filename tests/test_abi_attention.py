@@ -129,7 +129,7 @@ def test_rope_refusals():
     for axes in (0, 5, -1):
         assert rope(axes=axes) == INVALID, axes
     assert rope(axis=[2] * 64) == INVALID and rope(axis=[-1] * 64) == INVALID and rope(axis="null") == INVALID
-    assert rope(T=-1) == INVALID and rope(T=1 << 31) == INVALID and rope(H=-1) == INVALID
+    assert rope(T=-1) == INVALID and rope(T=1 << 22) == INVALID and rope(H=-1) == INVALID
     for kw in (dict(q=None), dict(out=None), dict(k=None), dict(v=None), dict(pos=None), dict(freq=None), dict(slots=None)):
         assert rope(**kw) == INVALID, kw
     for kw in (dict(q=P + 8), dict(k=P + 2), dict(v=P + 4), dict(out=P + 8), dict(qt=2056), dict(kt=520), dict(oh=8)):
@@ -142,7 +142,7 @@ def select(m=P, w=500, R=3, H=2, lens=P, budget=100, sink=4, recent=10, keep=P, 
 
 
 def test_select_refusals():
-    for kw in (dict(R=-1), dict(H=0), dict(w=-1), dict(budget=0), dict(budget=1 << 31), dict(sink=-1), dict(recent=-1),
+    for kw in (dict(R=-1), dict(R=1 << 21), dict(H=0), dict(w=-1), dict(budget=0), dict(budget=1 << 31), dict(sink=-1), dict(recent=-1),
                dict(sink=101), dict(sink=50, recent=51), dict(m=None), dict(lens=None), dict(keep=None), dict(new=None),
                dict(new=P)):
         assert select(**kw) == INVALID, kw
@@ -161,7 +161,7 @@ def test_compact_refusals():
         assert compact(c=cache(**kw)) == INVALID, kw
     for kw in ODD_CACHES:
         assert compact(c=cache(**kw)) == MISALIGNED, kw
-    for kw in (dict(R=-1), dict(H=0), dict(H=3), dict(budget=0), dict(cols=9), dict(drow=7), dict(src=None), dict(dst=None),
+    for kw in (dict(R=-1), dict(R=1 << 20), dict(H=0), dict(H=3), dict(budget=0), dict(cols=9), dict(drow=7), dict(src=None), dict(dst=None),
                dict(keep=None), dict(m=P), dict(mo=P), dict(m=P, mo=2 * P, w=-1), dict(m=P, mo=2 * P, wo=-1),
                dict(m=P, mo=P),  # onto itself, but not in place
                dict(dst=P, m=P, mo=P, mos=400), dict(dst=P, dcols=7), dict(c=cache(base=None)),
