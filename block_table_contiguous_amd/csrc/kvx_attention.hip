@@ -734,7 +734,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
 }
 
 // Joins the parts of a tile: out = sum_s 2^(lse_s - top) o_s / sum_s 2^(lse_s - top). A thread takes four
-// dimensions of one row, and with many parts only every fourth or eighth of them, the threads of a row and
+// dimensions of one row, and with many parts only every second or eighth of them, the threads of a row and
 // dimension side by side. What bounds it is one chain of loads: the batch, then the parts.
 template <class E, int ROWS, int BN>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, Split sp) {
@@ -755,7 +755,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, Split sp) {
   Rows x = q.x;
   x.tile = tile - q.tile0;
   const int rows = x.tokens * group - x.tile * ROWS, items = (rows < ROWS ? rows : ROWS) * quads;
-  const int ways_log = s_to - s_from <= 3 ? 0 : s_to - s_from <= 16 ? 2 : 3;
+  const int ways_log = s_to - s_from <= 8 ? 0 : s_to - s_from <= 16 ? 1 : 3;
   const int ways = 1 << ways_log, per = 256 >> ways_log, way = tid >> (8 - ways_log);
   for (int at = blockIdx.y * per; at < items; at += gridDim.y * per) {
     const int item = at + (tid & (per - 1)), row = item / quads, e = (item - row * quads) * 4;
@@ -866,8 +866,15 @@ void launch_attend(const AttendArgs& a, BlockDiv div, const Split& sp, bool keys
     return;
   }
   const dim3 grid((unsigned)(sp.shares * heads));
+  // A tile's rows are joined by one workgroup, or by several while that is up to 2048 in all (one round of them on
+  // the CUs) and they have 32 threads' work each: each first finds its tile again, so more cost more than they read.
   const int64_t blocks = (int64_t)sp.tiles * heads;
-  const dim3 join((unsigned)blocks, blocks >= 4096 ? 1u : (unsigned)(4096 / blocks < 16 ? 4096 / blocks : 16));
+  const int64_t longest = a.batch.max_query_len < a.batch.num_tokens ? a.batch.max_query_len : a.batch.num_tokens;
+  const int64_t most = longest * (a.num_heads / heads) * a.cache.head_dim / 128;
+  int64_t several = 2048 / blocks;
+  several = several < most ? several : most;
+  several = several < 1 ? 1 : several < 16 ? several : 16;
+  const dim3 join((unsigned)blocks, (unsigned)several);
   if (keys) {
     attend_kernel<E, DP, true, false, true><<<grid, 256, 0, stream>>>(a, div, sp);
     join_kernel<E, 32, 128><<<join, 256, 0, stream>>>(a, sp);
