@@ -917,7 +917,7 @@ __device__ __forceinline__ bool mass_rows(const MassArgs& ma, int r, int group, 
 // Loads a tile of rows as the memory holds them, 16 consecutive bytes a lane and whole rows by
 // neighbouring lanes, and passes it through LDS to the lanes that the products want it in: read
 // by those lanes directly, each would touch a line of its own, and the address unit, not
-// memory, would set the pace (a decode batch's masses: 108 us against 60).
+// memory, would set the pace (a decode batch's masses: 108 us against 92).
 template <int DP, int TILE>
 struct RowTile {
   static constexpr int VPR = DP / 8, RPI = 64 / VPR, NI = TILE / RPI, ROW = DP * 2 + 16;
@@ -933,7 +933,72 @@ struct RowTile {
     const int c = lane % VPR;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-      *(u32x4*)(lds + (i * RPI + lane / VPR) * ROW + c * 16) = VPR == vecs || c < vecs ? v[i] : u32x4{0, 0, 0, 0};
+      *(u32x4*)(lds + (i * RPI + lane / VPR) * ROW + c * 16) = v[i];
+    if (c >= vecs) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) *(u32x4*)(lds + (i * RPI + lane / VPR) * ROW + c * 16) = u32x4{0, 0, 0, 0};
+    }
+  }
+};
+
+// A lane's way through the rows (token, head of the group) of one KV head: found by a division once, and by a
+// comparison from then on, as the rows pass by in equal steps. Divided anew, the rows of a tile took
+// half as many instructions as its weights (61 tokens of 32 heads over 32749 slots 48 -> 45 us; a prompt's
+// 8192 tokens of 8 heads 558 -> 345 us).
+struct RowWalk {
+  int32_t token, head;
+  int64_t off;  // in bytes, from the request's first row
+  __device__ __forceinline__ void start(int row, int group, int64_t token_stride, int64_t head_stride) {
+    token = row / group;
+    head = row - token * group;
+    off = token * token_stride + head * head_stride;
+  }
+  __device__ __forceinline__ void advance(int rows, int group, int64_t token_stride, int64_t head_stride) {
+    const int tokens = rows / group, heads = rows - tokens * group;  // the same in every lane
+    const int64_t by = tokens * token_stride + heads * head_stride;
+    head += heads;
+    const bool over = head >= group;
+    head -= over ? group : 0;
+    token += over ? tokens + 1 : tokens;
+    off += over ? by + token_stride - group * head_stride : by;
+  }
+};
+// The rows of the mass kernels' loops.
+template <class Q>
+struct RowLoads {
+  const char *query, *lse;  // the request's first row's
+  int64_t lse_stride;       // of a token
+  int32_t first_end, window;  // the first token sees slots up to first_end
+  RowWalk qs, ls;
+  __device__ __forceinline__ void setup(const AttendArgs& a, const Rows& x, int g, int group) {
+    query = a.query.base + x.q0 * a.query.token_stride + (int64_t)g * group * a.query.head_stride;
+    lse = (const char*)(a.lse + x.q0 * a.num_heads + g * group);
+    lse_stride = (int64_t)a.num_heads * 4;
+    first_end = x.context - x.tokens + 1;
+    window = a.window < 0x7fffffff ? (int32_t)a.window : 0x7fffffff;
+  }
+  // row: of the tile's rows, the first that this lane loads a piece of; mine: the one whose weights it forms
+  __device__ __forceinline__ void start(const AttendArgs& a, int group, int row, int mine) {
+    qs.start(row, group, a.query.token_stride, a.query.head_stride);
+    ls.start(mine, group, lse_stride, 4);
+  }
+  // Loads tile rows from row on; left: of the rows from that one on, those that there are; a row past
+  // the last reads the first token's and sees nothing. Then on by step rows.
+  __device__ __forceinline__ void load(const AttendArgs& a, const Rows& x, int group, int lane, int vecs, int left, int n,
+                                       int first, int step, Q& q, int2* see, float* l) {
+    RowWalk w = qs;
+    q.load([&](int i) {
+      const int64_t off = first + i * Q::RPI + lane / Q::VPR < left ? w.off : 0;
+      w.advance(Q::RPI, group, a.query.token_stride, a.query.head_stride);
+      return query + off;
+    }, lane, vecs);
+    qs.advance(step, group, a.query.token_stride, a.query.head_stride);
+    const bool used = n < left;
+    *l = gload<float>((const float*)(lse + (used ? ls.off : 0)));
+    int hi = a.causal ? first_end + ls.token : x.context;
+    hi = hi < 0 || !used ? 0 : hi;
+    *see = {hi > window ? hi - window : 0, hi};
+    ls.advance(step, group, lse_stride, 4);
   }
 };
 
@@ -1010,6 +1075,8 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void mass_kernel(MassArgs m
   const Rows& x = m.x;
   const float c1 = a.scale * kLog2e;
   const int32_t* const table = a.batch.block_table + r * a.batch.bt_row_stride;
+  RowLoads<QTile> rows;
+  rows.setup(a, x, g, group);
   char* const own = smem + w * OWN;       // K on its way to registers, then partial sums
   char* const qs = smem + 4 * OWN;        // two tiles of query rows
   int errs = 0;
@@ -1056,20 +1123,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void mass_kernel(MassArgs m
     QTile q;
     int2 see;
     float lse;
-    auto row_of = [&](int row, int* token, int* head) {  // a row past the last reads the first token's
-      *token = row < row_to ? row / group : 0;
-      *head = g * group + (row < row_to ? row - *token * group : 0);
-    };
+    rows.start(a, group, row_from + w * 8 + lane / QTile::VPR, row_from + n);
     auto load_rows = [&](int row0) {
-      q.load([&](int i) {
-        int token, head;
-        row_of(row0 + w * 8 + i * QTile::RPI + lane / QTile::VPR, &token, &head);
-        return a.query.base + (x.q0 + token) * a.query.token_stride + head * a.query.head_stride;
-      }, lane, vecs);
-      int token, head;
-      row_of(row0 + n, &token, &head);
-      lse = gload<float>(a.lse + (x.q0 + token) * a.num_heads + head);
-      see = row0 + n < row_to ? sees(a, x, token) : int2{0, 0};
+      rows.load(a, x, group, lane, vecs, row_to - row0, n, w * 8, 32, q, &see, &lse);
     };
     // The products of one tile of rows run while the weights of the one before are formed.
     f32x16 s[2][2];
@@ -1130,30 +1186,34 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void mass_kernel(MassArgs m
   if (errs) raise(a.err, errs);
 }
 
-// The same where there are too few slots to fill the GPU that way, as with a whole prompt's rows: a workgroup's eight
+// The same where there are too few slots to fill the GPU that way, as with a whole prompt's rows: a workgroup's
 // wavefronts share 64 slots and take the tiles of rows in turn, each through LDS of its own; their sums
-// meet at the end, in order (a prompt of 8192 tokens of 8 heads on one KV head: 2084 -> 547 us).
-constexpr int kMassWaves = 8;
+// meet at the end, in order (a prompt of 8192 tokens of 8 heads on one KV head: 2084 us by mass_kernel, 345 so).
+// The widest heads have four, which leaves each the registers for its rows (1682 -> 839 us at 256).
+template <int DP>
+constexpr int kMassWaves = DP <= 128 ? 8 : 4;
 
 template <class E, int DP>
-__global__ __launch_bounds__(64 * kMassWaves, DP <= 128 ? 2 : 1) void mass_rows_kernel(MassArgs ma, BlockDiv div) {
-  typedef RowTile<DP, 64 / kMassWaves> KTile;  // a wavefront's share of 64 slots
+__global__ __launch_bounds__(64 * kMassWaves<DP>, DP <= 128 ? 2 : 1) void mass_rows_kernel(MassArgs ma, BlockDiv div) {
+  typedef RowTile<DP, 64 / kMassWaves<DP>> KTile;  // a wavefront's share of 64 slots
   typedef RowTile<DP, 32> QTile;
   constexpr int KSTEPS = DP / 16, LROW = 36, ROW = QTile::ROW;
   constexpr int OWN = 32 * ROW > 64 * LROW * 4 ? 32 * ROW : 64 * LROW * 4;
-  __shared__ __align__(16) char smem[kMassWaves * OWN];
-  __shared__ float sums[kMassWaves][64];
+  __shared__ __align__(16) char smem[kMassWaves<DP> * OWN];
+  __shared__ float sums[kMassWaves<DP>][64];
   const AttendArgs& a = ma.at;
   const int tid = threadIdx.x, lane = tid & 63, w = uniform((int32_t)(tid >> 6));
   const int n = lane & 31, hf = lane >> 5, g = blockIdx.x, r = blockIdx.z;
   const int group = a.num_heads / a.cache.num_kv_heads, vecs = a.cache.head_dim / 8;
   const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size;
-  if (blockIdx.y == 0 && g == 0 && r == 0) check_batch(a, cap, tid, 64 * kMassWaves);
+  if (blockIdx.y == 0 && g == 0 && r == 0) check_batch(a, cap, tid, 64 * kMassWaves<DP>);
   MassRows m;
   if (!mass_rows(ma, r, group, cap, &m)) return;
   const Rows& x = m.x;
   const float c1 = a.scale * kLog2e;
   const int32_t* const table = a.batch.block_table + r * a.batch.bt_row_stride;
+  RowLoads<QTile> rows;
+  rows.setup(a, x, g, group);
   char* const own = smem + w * OWN;
   int errs = 0;
 
@@ -1171,7 +1231,7 @@ __global__ __launch_bounds__(64 * kMassWaves, DP <= 128 ? 2 : 1) void mass_rows_
     {
       KTile t;
       const char* const base = (const char*)a.cache.base + g * a.cache.head_stride_bytes;
-      constexpr int SHARE = 64 / kMassWaves;
+      constexpr int SHARE = 64 / kMassWaves<DP>;
       t.load([&](int i) { return base + __shfl(off, w * SHARE + i * KTile::RPI + lane / KTile::VPR); }, lane, vecs);
       t.put(smem + w * SHARE * ROW, lane, vecs);
       lds_barrier();
@@ -1192,22 +1252,11 @@ __global__ __launch_bounds__(64 * kMassWaves, DP <= 128 ? 2 : 1) void mass_rows_
     QTile q;
     int2 see;
     float lse;
-    auto row_of = [&](int row, int* token, int* head) {  // a row past the last reads the first token's
-      *token = row < row_to ? row / group : 0;
-      *head = g * group + (row < row_to ? row - *token * group : 0);
-    };
+    rows.start(a, group, row_from + w * 32 + lane / QTile::VPR, row_from + w * 32 + n);
     auto load_rows = [&](int row0) {
-      q.load([&](int i) {
-        int token, head;
-        row_of(row0 + i * QTile::RPI + lane / QTile::VPR, &token, &head);
-        return a.query.base + (x.q0 + token) * a.query.token_stride + head * a.query.head_stride;
-      }, lane, vecs);
-      int token, head;
-      row_of(row0 + n, &token, &head);
-      lse = gload<float>(a.lse + (x.q0 + token) * a.num_heads + head);
-      see = row0 + n < row_to ? sees(a, x, token) : int2{0, 0};
+      rows.load(a, x, group, lane, vecs, row_to - row0, n, 0, 32 * kMassWaves<DP>, q, &see, &lse);
     };
-    constexpr int STEP = 32 * kMassWaves;
+    constexpr int STEP = 32 * kMassWaves<DP>;
     int row0 = row_from + w * 32;
     if (row0 < row_to) load_rows(row0);
     for (; row0 < row_to; row0 += STEP) {
@@ -1233,7 +1282,7 @@ __global__ __launch_bounds__(64 * kMassWaves, DP <= 128 ? 2 : 1) void mass_rows_
       float* const mass = ma.mass + r * ma.mass_req_stride + g * ma.mass_head_stride + j;
       float t = 0;
 #pragma unroll
-      for (int i = 0; i < kMassWaves; ++i) t += sums[i][lane];
+      for (int i = 0; i < kMassWaves<DP>; ++i) t += sums[i][lane];
       gstore(mass, gload<float>(mass) + t);
     }
     lds_barrier();
@@ -1366,7 +1415,7 @@ enum { kMassBySlots, kMassByRows, kMassFew };
 template <class E, int DP>
 void launch_mass_dim(const MassArgs& m, BlockDiv div, dim3 grid, int how, int span, hipStream_t stream) {
   if (how == kMassFew) mass_few_kernel<E, DP><<<grid, 256, 0, stream>>>(m, div, span);
-  else if (how == kMassByRows) mass_rows_kernel<E, DP><<<grid, 64 * kMassWaves, 0, stream>>>(m, div);
+  else if (how == kMassByRows) mass_rows_kernel<E, DP><<<grid, 64 * kMassWaves<DP>, 0, stream>>>(m, div);
   else mass_kernel<E, DP><<<grid, 256, 0, stream>>>(m, div);
 }
 
