@@ -181,6 +181,14 @@ def test_masses_of_a_large_batch(dim):
     run(case, window=0 if dim == 64 else 600)
 
 
+@pytest.mark.parametrize("heads,kv,dim", [(33, 1, 64), (14, 2, 128), (3, 1, 136)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_masses_of_head_groups(heads, kv, dim, causal):
+    """Groups that the tiles of 32 rows do not divide, over many tiles, in the same launch as short requests."""
+    run(A.Case(36, [(60, 900)] * (150 // kv) + [(97, 97), (11, 1000)], heads=heads, kv_heads=kv, dim=dim, extra=2), causal=causal,
+        window=333 if causal else 0)
+
+
 @pytest.mark.parametrize("dim,dtype", [(80, "bf16"), (256, "fp16")])
 def test_shared_work_of_other_dims(dim, dtype):
     run(A.Case(30, [(1, 6000), (1, 200), (1, 3001)], heads=4, kv_heads=1, dim=dim, dtype=dtype))
