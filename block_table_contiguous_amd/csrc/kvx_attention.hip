@@ -301,7 +301,15 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   const int n = lane & 31, hf = lane >> 5;
   const int group = a.num_heads / a.cache.num_kv_heads, vecs = a.cache.head_dim / 8;
   const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size;
-  const int g = blockIdx.x % a.cache.num_kv_heads, index = blockIdx.x / a.cache.num_kv_heads;
+  // Workgroup i runs on XCD i % 8, each with an L2 of its own: a head's tiles, or shares that follow one another and read
+  // the same K and V, to one XCD (8 requests' chunks on one KV head 129 -> 124 us).
+  int g = blockIdx.x % a.cache.num_kv_heads, index = blockIdx.x / a.cache.num_kv_heads;
+  if constexpr (SHARED) {
+    const int xcd = blockIdx.x % 8, per = gridDim.x / 8, more = gridDim.x % 8;
+    const int at = xcd * per + (xcd < more ? xcd : more) + blockIdx.x / 8;
+    g = at / sp.shares;
+    index = at - g * sp.shares;
+  }
   if (blockIdx.x == 0) check_batch(a, cap, tid, 256);
 
   // the padding of every row is zero, once
