@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import List, Optional, Sequence
 
 import numpy as np
@@ -92,7 +93,7 @@ SIGNATURES = {
     "kvx_pack_signal_noalloc": (ctypes.c_int, [_P, _I32, _I64, _I64, _P, _P, _I64, _P, _P, ctypes.c_uint64, _I32,
                                                _P, _P]),
     "kvx_rope_and_cache": (ctypes.c_int, [_CACHE, _P, _I64, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _I32,
-                                          ctypes.POINTER(_I32), _P, _I32, _I32, _P, _P, _I64, _I64, _P, _P]),
+                                          _P, _P, _I32, _I32, _P, _P, _I64, _I64, _P, _P]),
     "kvx_paged_attention": (ctypes.c_int, [_CACHE, _BATCH, _P, _I64, _I64, _I32, _F32, _I32, _I64, _P, _I64, _I64, _P,
                                            _P, _I64, _P, _P]),
     "kvx_paged_attention_workspace": (_I64, [_CACHE, _BATCH, _I32]),
@@ -716,9 +717,10 @@ def kvx_rope_and_cache(query, key, value, positions, inv_freq, pair_axis: Sequen
         os_ = _rows(query_out, T, heads, c, "query_out")
         q_ptr, o_ptr = query.data_ptr(), query_out.data_ptr()
     _on_current_device((query, key, value, positions, inv_freq, slot_mapping, c.tensor, query_out, err_flag))
+    axis_of = array("i", pair_axis if pairs else (0,))  # a ctypes array of as many costs three times this
     st = _F["kvx_rope_and_cache"](
         c, q_ptr, *qs, heads, key.data_ptr(), *ks, value.data_ptr(), *vs, T, positions.data_ptr(), axes[0],
-        (_I32 * max(pairs, 1))(*pair_axis), inv_freq.data_ptr(), 2 * pairs, bool(interleaved), slot_mapping.data_ptr(),
+        axis_of.buffer_info()[0], inv_freq.data_ptr(), 2 * pairs, bool(interleaved), slot_mapping.data_ptr(),
         o_ptr, *os_, _ptr(err_flag), _stream(stream))
     _check("kvx_rope_and_cache", st)
 
