@@ -26,7 +26,7 @@ __device__ __forceinline__ uint32_t rank_of(float m) {
 // digit). The rank of the last kept slot is found digit by digit from the top: a histogram of 8
 // bits a round over the slots that agree with the digits found. Then the slots above it and the lowest ones that
 // equal it are written in order, their places from counts by wavefront and 64 slots. What bounds it
-// is the chain of rounds, each a pass through LDS (8 x 8 lists of 9216: 24 -> 15 us with the registers).
+// is the chain of rounds, each a pass through LDS (8 x 8 lists of up to 9216: 24 -> 15 us with the registers).
 constexpr int kSelRegs = 16;
 constexpr int kSelSlots = kSelRegs * kSelThreads;
 constexpr int kSelCopies = 4;  // histograms, by wavefront: equal digits of different wavefronts do not collide

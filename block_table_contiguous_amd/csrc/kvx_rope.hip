@@ -6,7 +6,7 @@
 // functions themselves then take the fraction in 32 bits. The rows are moved as 16-byte vectors,
 // a thread holding both halves of its pairs; each is read and written once, and that is the bound:
 // HBM bytes for many tokens, one launch and two dependent loads for a few. The first rows are on their
-// way while the angles are formed, and the next ones while a thread turns its own (16384
+// way while the angles are formed, and the next ones while a thread turns its own (9461
 // tokens of 32 + 8 heads of 128: 233 MB in 45 us). Stores go by the caches' default policy: the attention reads
 // the rows next.
 #include <hip/hip_runtime.h>

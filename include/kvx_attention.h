@@ -95,7 +95,7 @@ typedef struct kvx_batch {
  *              in 64 bits.
  *   slot_mapping int64 [num_tokens]: slot < 0 writes no K and V (padding); a slot in a block >=
  *              num_blocks is skipped and raises KVX_DEVERR_SLOT_RANGE. The query is rotated either
- *              way.
+ *              way. Two tokens of a call must not have the same slot.
  * num_heads may be 0 (query NULL) to rotate and write keys alone. rot_dim is a multiple of 16,
  * 16 <= rot_dim <= head_dim. Errors: INVALID_ARGUMENT, MISALIGNED.
  */
@@ -159,7 +159,7 @@ int64_t kvx_paged_attention_workspace(const kvx_paged_cache* cache, const kvx_ba
  *   lse is -inf give nothing. Slots no row sees keep their bits.
  *   mass   float32 [num_reqs][num_kv_heads][mass_width] at the given strides (in floats, the last
  *          dimension dense); a context longer than mass_width raises KVX_DEVERR_TABLE_RANGE and
- *          is cut there.
+ *          is cut there. With mass_width or max_blocks_per_req 0 the call does nothing.
  * Only K is read. The last tokens of a prompt, or each decoded token in turn, are what callers
  * usually accumulate over.
  */
