@@ -180,7 +180,10 @@ __device__ __forceinline__ void loads_landed() {
 __global__ __launch_bounds__(kMoveThreads) void compact_kernel(CompactArgs a, BlockDiv div) {
   const kvx_paged_cache& cache = a.cache;
   const int columns = 2 * cache.num_kv_heads + (a.mass ? a.num_heads : 0);
-  const int r = blockIdx.x / columns, col = blockIdx.x - r * columns;
+  // Workgroup i runs on XCD i % 8: a request's columns, whose rows lie side by side, to one XCD where they can be (72 -> 70 us)
+  const int xcd = blockIdx.x % 8, per = gridDim.x / 8, more = gridDim.x % 8;
+  const int at_column = xcd * per + (xcd < more ? xcd : more) + blockIdx.x / 8;
+  const int r = at_column / columns, col = at_column - r * columns;
   const int tid = threadIdx.x;
   const bool in_place = a.src_table == a.dst_table;
   int errs = 0;
