@@ -526,15 +526,18 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
     const uint8_t flag = flags[kw + (lane & (KT * 32 - 1))];
     // one bit a slot of this wavefront; with KEYS its 32 slots are read twice
     const uint64_t there = __ballot(flag & 1), skipped = __ballot((flag & 2) && lane < KT * 32);
+    // The wavefront that has begun on a tile goes first until it is done: the SIMD's other one does its own part better
+    // while these products run (1192 -> 1122 us at 2048 queries of 32 heads over 32768 slots from the weights on, 1112 from here).
+    __builtin_amdgcn_s_setprio(1);
     f32x16 s[KT];
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      s[kt] = f32x16{};
+    for (int kt = 0; kt < KT; ++kt) s[kt] = f32x16{};
 #pragma unroll
-      for (int st = 0; st < KSTEPS; ++st)
+    for (int st = 0; st < KSTEPS; ++st)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)  // no product waits for the one before it
         s[kt] = mfma(E(), *(const u32x4*)(sk_get + kt * 32 * KROW + st * 32),
                      Q_LDS ? *(const u32x4*)(sq + st * 32) : q[Q_LDS ? 0 : st], s[kt]);
-    }
     // K is read eight pieces ahead of the products: read as they are needed, each would wait for LDS
     if constexpr (!Q_LDS) {
     __builtin_amdgcn_sched_group_barrier(kDsRead, 8, 0);
@@ -577,10 +580,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
     }
     const float ref = m == -INFINITY ? 0.0f : m;
     // Weights and products by 16 slots: V is read one group ahead, and the weights of a group are
-    // formed in the shadow of the products of the one before. The wavefront that is here goes first: the
-    // SIMD's other one does its own part better while these products run (1177 -> 1125 us at 2048
-    // queries of 32 heads over 32768 slots).
-    __builtin_amdgcn_s_setprio(1);
+    // formed in the shadow of the products of the one before.
 #pragma unroll
     for (int gr = 0; gr < 2 * KT; ++gr) {
       f32x8 pv;
