@@ -23,139 +23,142 @@ __device__ __forceinline__ uint32_t rank_of(float m) {
 }
 
 // One workgroup a list. The masses are read once, into registers (lists beyond kSelSlots in pieces, again for every
-// digit). The rank of the last kept slot is found digit by digit from the top: a histogram of 8
-// bits a round over the slots that agree with the digits found. Then the slots above it and the lowest ones that
-// equal it are written in order, their places from counts by wavefront and 64 slots. What bounds it
-// is the chain of rounds, each a pass through LDS (8 x 8 lists of up to 9216: 24 -> 15 us with the registers).
-constexpr int kSelRegs = 16;
+// digit). The rank of the last kept slot is found digit by digit from the top, 11, 11 and 10 bits: a histogram a round
+// over the slots that agree with the digits found. A digit of 11 bits spreads masses of like size, which share sign and
+// exponent, over some bins: the additions of a wavefront to one bin come one after the other.
+// Then the slots above the rank and the lowest ones that equal it are written in order, their places from counts by wavefront
+// and 64 slots. What bounds it is the chain of rounds, each a pass through LDS (8 x 8 lists of 9216: 13.2 us, 17.6 with
+// four digits of 8 bits; 8 lists of 32768: 27 us, 62 with half as many registers and four digits).
+constexpr int kSelRegs = 32;
 constexpr int kSelSlots = kSelRegs * kSelThreads;
-constexpr int kSelCopies = 4;  // histograms, by wavefront: equal digits of different wavefronts do not collide
+constexpr int kSelBins = 2048;
+constexpr int kSelCopies = 2;  // histograms, by wavefront: equal digits of different wavefronts collide less
 
 __global__ __launch_bounds__(kSelThreads) void select_kernel(SelectArgs a) {
-  __shared__ uint32_t hist[kSelCopies][256];
+  __shared__ __align__(16) uint32_t hist[kSelCopies][kSelBins];
+  __shared__ uint32_t tops[kSelWaves];
   __shared__ uint32_t counts[2][kSelRegs * kSelWaves];  // above the rank, equal to it: of 64 slots each, in order
   __shared__ uint32_t found[4];  // digit, slots still wanted among those that have it; totals of a piece
   const int r = blockIdx.x / a.num_heads, h = blockIdx.x - r * a.num_heads;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t c = a.context_lens[r];
   const int64_t clamped = c < 0 ? 0 : c > a.width ? a.width : c;
   if (c != clamped && tid == 0) raise(a.err, KVX_DEVERR_TABLE_RANGE);
-  const int n = (int)clamped, want_all = n < a.budget ? n : a.budget;
+  const uint32_t n = (uint32_t)clamped, budget = (uint32_t)a.budget, want_all = n < budget ? n : budget;
   if (h == 0 && tid == 0) a.new_lens[r] = want_all;
   int32_t* keep = a.keep + (int64_t)blockIdx.x * a.budget;
-  if (n <= a.budget) {
-    for (int64_t i = tid; i < a.budget; i += kSelThreads) keep[i] = i < n ? (int32_t)i : -1;
+  if (n <= budget) {
+    for (uint32_t i = tid; i < budget; i += kSelThreads) keep[i] = i < n ? (int32_t)i : -1;
     return;
   }
   const float* mass = a.mass + r * a.req_stride + h * a.head_stride;
-  const int last = n - a.recent;
+  const uint32_t last = n - (uint32_t)a.recent, sink = (uint32_t)a.sink;
   uint32_t k[kSelRegs];
-  auto load = [&](int64_t j0) {
+  auto load = [&](uint32_t j0) {
     float m[kSelRegs];
 #pragma unroll
     for (int i = 0; i < kSelRegs; ++i) {
-      const int64_t j = j0 + i * kSelThreads + tid;
+      const uint32_t j = j0 + i * kSelThreads + tid;
       if (j - tid < n) m[i] = gload<float>(mass + (j < n ? j : 0));
     }
 #pragma unroll
     for (int i = 0; i < kSelRegs; ++i) {
-      const int64_t j = j0 + i * kSelThreads + tid;
-      if (j - tid < n) k[i] = j < a.sink || j >= last ? 0xffffffffu : rank_of(m[i]);
+      const uint32_t j = j0 + i * kSelThreads + tid;
+      if (j - tid < n) k[i] = j < sink || j >= last ? 0xffffffffu : rank_of(m[i]);
     }
   };
   load(0);
-  uint32_t prefix = 0, mask = 0, want = (uint32_t)want_all;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    (&hist[0][0])[tid] = 0;
+  uint32_t prefix = 0, mask = 0, want = want_all;
+  for (int shift = 21;; shift = shift > 11 ? shift - 11 : 0) {
+    *(u32x4*)(&hist[0][0] + 4 * tid) = u32x4{0, 0, 0, 0};
     __syncthreads();
-    for (int64_t j0 = 0; j0 < n; j0 += kSelSlots) {
+    for (uint32_t j0 = 0; j0 < n; j0 += kSelSlots) {
       if (n > kSelSlots) load(j0);
 #pragma unroll
       for (int i = 0; i < kSelRegs; ++i) {
-        const int64_t j = j0 + i * kSelThreads + tid;
+        const uint32_t j = j0 + i * kSelThreads + tid;
         if (j - tid >= n) break;
-        if (j < n && (k[i] & mask) == prefix) atomicAdd(&hist[wave % kSelCopies][(k[i] >> shift) & 255], 1u);
+        if (j < n && (k[i] & mask) == prefix) atomicAdd(&hist[wave % kSelCopies][(k[i] >> shift) & (kSelBins - 1)], 1u);
       }
     }
     __syncthreads();
-    if (wave == 0) {  // lane l: bins 255-4l .. 252-4l, from the largest down
-      uint32_t b[4], sum = 0;
-      for (int i = 0; i < 4; ++i) {
-        b[i] = 0;
-        for (int v = 0; v < kSelCopies; ++v) b[i] += hist[v][255 - 4 * lane - i];
-        sum += b[i];
-      }
-      uint32_t upto = sum;
-      for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t o = __shfl_up(upto, d);
-        if (lane >= d) upto += o;
-      }
-      uint32_t before = upto - sum;
-      for (int i = 0; i < 4; ++i) {
-        if (before < want && want <= before + b[i]) {
-          found[0] = 255 - 4 * lane - i;
-          found[1] = want - before;
-        }
-        before += b[i];
-      }
+    // this thread: two bins, from the largest down
+    const uint32_t bin = kSelBins - 2 - 2 * tid;
+    uint32_t high = 0, low = 0;
+#pragma unroll
+    for (int v = 0; v < kSelCopies; ++v) {
+      const u32x2 b = *(const u32x2*)&hist[v][bin];
+      low += b[0];
+      high += b[1];
+    }
+    uint32_t upto = high + low;
+    for (uint32_t d = 1; d < 64; d <<= 1) {
+      const uint32_t o = __shfl_up(upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 63) tops[wave] = upto;
+    __syncthreads();
+    uint32_t before = upto - high - low;
+    for (uint32_t v = 0; v < wave; ++v) before += tops[v];
+    if (before < want && want <= before + high + low) {
+      const bool first = want <= before + high;
+      found[0] = bin + first;
+      found[1] = want - before - (first ? 0 : high);
     }
     __syncthreads();
-    prefix |= found[0] << shift;
-    mask |= 255u << shift;
+    prefix |= found[0] << shift;  // the last digit's top bit is the one before's lowest
+    mask |= (uint32_t)(kSelBins - 1) << shift;
     want = found[1];
+    if (shift == 0) break;
   }
   uint32_t base = 0, ties = want;  // slots written so far; equal slots still to write
-  for (int64_t j0 = 0; j0 < n; j0 += kSelSlots) {
+  for (uint32_t j0 = 0; j0 < n; j0 += kSelSlots) {
     if (n > kSelSlots) load(j0);
-    uint64_t gt[kSelRegs], eq[kSelRegs];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kSelRegs; ++i) {
-      const int64_t j = j0 + i * kSelThreads + tid;
-      if (j - tid >= n) {  // this row of 1024 slots and the ones after it are behind the list
-        gt[i] = eq[i] = 0;
-        if (lane < 2) counts[lane][i * kSelWaves + wave] = 0;
-        continue;
-      }
-      gt[i] = __ballot(j < n && k[i] > prefix);
-      eq[i] = __ballot(j < n && k[i] == prefix);
-      if (lane == 0) {
-        counts[0][i * kSelWaves + wave] = __popcll(gt[i]);
-        counts[1][i * kSelWaves + wave] = __popcll(eq[i]);
-      }
+      const uint32_t j = j0 + i * kSelThreads + tid;
+      if (j - tid >= n) break;  // this row of 1024 slots and the ones after it are behind the list
+      const uint32_t above = __popcll(__ballot(j < n && k[i] > prefix));
+      const uint32_t equal = __popcll(__ballot(j < n && k[i] == prefix));
+      if (lane < 2) counts[lane][i * kSelWaves + wave] = lane ? equal : above;
     }
     __syncthreads();
-    if (wave < 2) {  // each count becomes the sum of those before it: lane l's are 4l .. 4l+3
-      uint32_t* const at = counts[wave] + 4 * lane;
-      uint32_t v[4], sum = 0;
-      for (int i = 0; i < 4; ++i) {
+    if (wave < 2) {  // each count becomes the sum of those before it: lane l's are kEach l .. kEach l + kEach - 1
+      constexpr int kEach = kSelRegs * kSelWaves / 64;
+      uint32_t* const at = counts[wave] + kEach * lane;
+      const uint32_t written = (n - j0 + kSelThreads - 1) / kSelThreads * kSelWaves;
+      uint32_t v[kEach], sum = 0;
+      for (int i = 0; i < kEach; ++i) {
         v[i] = sum;
-        sum += at[i];
+        sum += kEach * lane + i < written ? at[i] : 0;
       }
       uint32_t upto = sum;
-      for (int d = 1; d < 64; d <<= 1) {
+      for (uint32_t d = 1; d < 64; d <<= 1) {
         const uint32_t o = __shfl_up(upto, d);
         if (lane >= d) upto += o;
       }
-      for (int i = 0; i < 4; ++i) at[i] = v[i] + upto - sum;
+      for (int i = 0; i < kEach; ++i) at[i] = v[i] + upto - sum;
       if (lane == 63) found[2 + wave] = upto;
     }
     __syncthreads();
     const uint64_t under = (1ull << lane) - 1;
 #pragma unroll
     for (int i = 0; i < kSelRegs; ++i) {
-      if (j0 + i * kSelThreads >= n) break;
-      const uint32_t g = counts[0][i * kSelWaves + wave] + __popcll(gt[i] & under);
-      const uint32_t e = counts[1][i * kSelWaves + wave] + __popcll(eq[i] & under);
-      if (((gt[i] >> lane) & 1) || (((eq[i] >> lane) & 1) && e < ties))
-        keep[base + g + (e < ties ? e : ties)] = (int32_t)(j0 + i * kSelThreads + tid);
+      const uint32_t j = j0 + i * kSelThreads + tid;
+      if (j - tid >= n) break;
+      const bool gt = j < n && k[i] > prefix, eq = j < n && k[i] == prefix;
+      const uint32_t g = counts[0][i * kSelWaves + wave] + __popcll(__ballot(gt) & under);
+      const uint32_t e = counts[1][i * kSelWaves + wave] + __popcll(__ballot(eq) & under);
+      if (gt || (eq && e < ties)) keep[base + g + (e < ties ? e : ties)] = (int32_t)j;
     }
     const uint32_t e_kept = found[3] < ties ? found[3] : ties;
     base += found[2] + e_kept;
     ties -= e_kept;
   }
 }
-static_assert(kSelRegs * kSelWaves == 256 && kSelCopies * 256 == kSelThreads, "one entry a thread or four a lane");
+static_assert(kSelRegs * kSelWaves % 64 == 0 && kSelBins == 2 * kSelThreads && kSelCopies * kSelBins == 4 * kSelThreads,
+              "two bins and four entries a thread, whole counts a lane");
 
 // --------------------------------------------------------------------------------------
 // moving

@@ -63,6 +63,15 @@ def test_select_lengths(n):
             check_select(mass, [n, max(0, n - 7)], budget, 2, budget // 2)
 
 
+@pytest.mark.parametrize("n", [1023, 16384, 16385, 32767, 32768, 32769, 65536, 70001])
+def test_select_long_lists(n):
+    """Around the slots that the registers hold at once, with ties across them and masses that share their leading bits."""
+    g = torch.Generator().manual_seed(n)
+    mass = torch.stack([torch.rand(n, generator=g) * 2.0 ** -20 + 1, torch.randint(0, 3, (n,), generator=g).float()])[None]
+    for budget in (1, 700, n // 2, n - 1):
+        check_select(mass, [n], budget, min(4, budget - 1), min(64, budget // 2))
+
+
 def test_select_ties_and_special_values():
     g = torch.Generator().manual_seed(3)
     ties = torch.randint(0, 4, (3, 2, 3000), generator=g).float()
