@@ -217,6 +217,16 @@ __device__ __forceinline__ float other_half(float x) {
   return __builtin_bit_cast(float, (threadIdx.x & 32) ? r[0] : r[1]);
 }
 
+// The reference that weights are formed against, 2^(x - m): kLift below the row's maximum when it is set, and left
+// there until the maximum stands kLift + kLag above it, so that weights end at 2^(kLift + kLag). fp16 ends at 2^16 and
+// rounds to steps of 2^-24 at the lower end: lifted, weights keep all their bits down to 2^-25 of the largest, and round
+// off by 2^-36 of it below (unlifted, a tail of slots that weigh less than 2^-25 each, as behind an attention sink, would be
+// lost whole). bf16 has the exponents of 32 bits and needs no lift.
+template <class E>
+constexpr float kLift = __is_same(E, Fp16) ? 11.0f : 0.0f;
+template <class E>
+constexpr float kLag = __is_same(E, Fp16) ? 4.0f : 8.0f;
+
 template <class E>
 __device__ __forceinline__ bool non_finite(u32x4 v) {
   constexpr uint32_t exp = sizeof(E) && __is_same(E, Bf16) ? 0x7f80u : 0x7c00u;
@@ -566,10 +576,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kt][i]);
     top = fmaxf(top, other_half(top)) * c1;
-    // The maximum that weights refer to moves only when it is exceeded by 2^8: no weight passes 2^8,
-    // and the sums keep their 32 bits.
-    if (__any(top > m + 8.0f)) {
-      const float to = top > m + 8.0f ? top : m;
+    // The reference moves only when the maximum leaves its range: the sums keep their 32 bits.
+    if (__any(top > m + (kLift<E> + kLag<E>))) {
+      const float to = top > m + (kLift<E> + kLag<E>) ? top - kLift<E> : m;
       const float shrink = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
       m = to;
       l *= shrink;

@@ -12,7 +12,10 @@
  *
  * Unlike the copies of kvx.h these calls do floating-point work. Elements are 16-bit (bf16 or
  * fp16); products are accumulated and softmax statistics, angles and totals held in 32 bits
- * (angles in 64), and results are rounded to the element type once, to nearest even. Every
+ * (angles in 64), and results are rounded to the element type once, to nearest even. One more
+ * rounding is in kvx_paged_attention: the matrix units take the weights that multiply V in the
+ * element type, so each is off by up to half a step (bf16 2^-8, fp16 2^-11; fp16 weights below 2^-25
+ * of their row's largest by up to 2^-36 of that one), while the sum that divides them holds them unrounded. Every
  * result is a fixed function of the inputs and the launch parameters: there are no atomics on
  * results, and a repeated call gives the same bits.
  */
