@@ -3,6 +3,7 @@
 #include <stdint.h>
 
 #include "kvx_attention_launch.h"
+#include "kvx_attention_plan.h"
 #include "kvx_paged.h"
 
 namespace kvx {
@@ -834,41 +835,6 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, Split sp) {
   }
 }
 
-// The launch shape of a batch: by slots (KEYS) where a request's rows of one KV head fit one tile of
-// 32. Where the tiles alone do not fill the GPU with two workgroups a CU (kFill), or leave a decode
-// batch's uneven contexts to a few rounds of workgroups, they are shared out evenly to kFill
-// workgroups, of kMinSteps steps at least, if there is a workspace for the parts.
-constexpr int kFill = 512, kMinSteps = 4;
-constexpr int64_t kMaxContext = 0x7fffffff;
-
-struct Plan {
-  bool keys;
-  int32_t tiles, shares;
-};
-Plan plan_attention(const kvx_paged_cache& c, const kvx_batch& b, int32_t num_heads) {
-  const int64_t group = num_heads / c.num_kv_heads;
-  const int64_t longest = b.max_query_len < b.num_tokens ? b.max_query_len : b.num_tokens;
-  Plan p;
-  p.keys = longest * group <= 32;
-  const int64_t rows = p.keys ? 32 : 128, slots = p.keys ? 128 : 64;
-  p.tiles = (int32_t)(b.num_tokens * group / rows + b.num_reqs);
-  int64_t busy = b.num_reqs * ((longest * group + rows - 1) / rows);
-  if (busy > p.tiles) busy = p.tiles;
-  if (busy < 1) busy = 1;
-  const int64_t context = b.max_context_len < kMaxContext ? b.max_context_len : kMaxContext;
-  const int fill = c.head_dim > 128 ? kFill / 2 : kFill;  // the widest heads' tiles leave room for one workgroup a CU
-  int64_t shares = fill / c.num_kv_heads, most = busy * (context / slots) / kMinSteps;
-  if (shares > most) shares = most;
-  const bool uneven = busy * c.num_kv_heads < (p.keys ? 4 * fill : fill);
-  p.shares = uneven && shares > (p.keys ? busy / 4 : busy) ? (int32_t)shares : 0;
-  return p;
-}
-
-// Bytes of a slot: a part of one tile of every KV head.
-int64_t slot_bytes(const kvx_paged_cache& c, bool keys) {
-  return (int64_t)c.num_kv_heads * (keys ? 32 : 128) * 4 * ((int64_t)c.head_dim + 1);
-}
-
 template <class E, int DP>
 void launch_attend(const AttendArgs& a, BlockDiv div, const Split& sp, bool keys, hipStream_t stream) {
   const int heads = a.cache.num_kv_heads;
@@ -1448,10 +1414,7 @@ void launch_mass_dims(const MassArgs& m, BlockDiv div, dim3 grid, int how, int s
 
 hipError_t launch_attention(const AttendArgs& a, hipStream_t stream) {
   const Plan p = plan_attention(a.cache, a.batch, a.num_heads);
-  Split sp = {p.shares, p.tiles, nullptr, nullptr};
-  // a workspace too small for the plan takes fewer shares, as long as they are worth it
-  const int64_t fit = a.workspace_bytes / slot_bytes(a.cache, p.keys) - p.tiles;
-  if (sp.shares > fit) sp.shares = fit > 1 ? (int32_t)fit : 0;
+  Split sp = {shares_within(p, a.cache, a.workspace_bytes), p.tiles, nullptr, nullptr};
   if (sp.shares > 0) {
     sp.acc = (float*)a.workspace;  // first: rows of 16-byte vectors
     sp.lse = sp.acc + (int64_t)(sp.shares + p.tiles) * a.cache.num_kv_heads * (p.keys ? 32 : 128) * a.cache.head_dim;

@@ -130,7 +130,8 @@ kvx_status kvx_rope_and_cache(const kvx_paged_cache* cache, const void* query,
  *   lse          float32 [num_tokens][num_heads], or NULL.
  *   workspace    device memory of workspace_bytes, 16-byte aligned, contents irrelevant, or NULL:
  *                lets the call split long contexts over more of the GPU and join the parts. With
- *                kvx_paged_attention_workspace() bytes it splits as far as pays, with fewer less far.
+ *                kvx_paged_attention_workspace() bytes it splits as far as pays, with fewer less far
+ *                or, where that would leave the GPU idle, not at all.
  *                Calls that may run at the same time, replayed graphs among them, need one each.
  *   scale        finite and > 0.
  * Rows that belong to nobody are left as they were. A context longer than the block table's row, a
