@@ -125,14 +125,17 @@ __device__ __forceinline__ void extent(const AttendArgs& a, const Rows& x, int g
   const int lo = sees(a, x, 0).x, hi = sees(a, x, x.tokens - 1).y;
   *steps = hi > lo ? (hi + BN - 1) / BN - lo / BN : 1;
 }
-// 64 requests of the batch, one a lane: their tiles and steps, and those of all requests before them.
+// 64 requests of the batch, one a lane: their tiles and steps, and those of all requests before them. Offsets that
+// give the same rows to many requests can make more tiles than 32 bits hold: tile0 then wraps around, and who takes a
+// tile's number for a place checks that there is one.
 struct Requests {
   Rows x;
-  int32_t tiles, steps, tile0;
+  int32_t tiles, steps;
+  uint32_t tile0;
   int64_t step0;
 };
 template <int ROWS, int BN>
-__device__ __forceinline__ Requests sixty_four(const AttendArgs& a, int group, int64_t cap, int lane, int r0, int32_t tile0,
+__device__ __forceinline__ Requests sixty_four(const AttendArgs& a, int group, int64_t cap, int lane, int r0, uint32_t tile0,
                                                int64_t step0) {
   Requests q = {};
   if (r0 + lane < a.batch.num_reqs) {
@@ -140,11 +143,11 @@ __device__ __forceinline__ Requests sixty_four(const AttendArgs& a, int group, i
     extent<ROWS, BN>(a, q.x, group, &q.tiles, &q.steps);
   }
   int64_t sum = (int64_t)q.tiles * q.steps;
-  int32_t num = q.tiles;
+  uint32_t num = q.tiles;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int64_t s = __shfl_up(sum, d);
-    const int32_t t = __shfl_up(num, d);
+    const uint32_t t = __shfl_up(num, d);
     if (lane >= d) sum += s, num += t;
   }
   q.tile0 = tile0 + num - q.tiles;
@@ -159,7 +162,7 @@ __device__ __forceinline__ Requests locate(const AttendArgs& a, int group, int64
   Requests q = {};
   const int reqs = a.batch.num_reqs;
   for (int r0 = 0; r0 < reqs; r0 += 64)
-    q = sixty_four<ROWS, BN>(a, group, cap, lane, r0, lane_of(q.tile0 + q.tiles, 63),
+    q = sixty_four<ROWS, BN>(a, group, cap, lane, r0, lane_of((int32_t)(q.tile0 + q.tiles), 63),
                              lane_of(q.step0 + (int64_t)q.tiles * q.steps, 63));
   all->steps = lane_of(q.step0 + (int64_t)q.tiles * q.steps, 63);
   all->count = all->steps < shares ? (int32_t)all->steps : shares;
@@ -169,13 +172,13 @@ __device__ __forceinline__ Requests locate(const AttendArgs& a, int group, int64
   Requests f = q;
   for (int r0 = 0;; r0 += 64) {
     if (reqs > 64)  // up to 64 requests the first pass holds them all
-      f = sixty_four<ROWS, BN>(a, group, cap, lane, r0, r0 ? lane_of(f.tile0 + f.tiles, 63) : 0,
+      f = sixty_four<ROWS, BN>(a, group, cap, lane, r0, r0 ? lane_of((int32_t)(f.tile0 + f.tiles), 63) : 0,
                                r0 ? lane_of(f.step0 + (int64_t)f.tiles * f.steps, 63) : 0);
     const uint64_t there = __ballot(f.tiles > 0 && holds(*all, f));
     if (there) {
       const int l = __builtin_ctzll(there);
       return {{r0 + l, lane_of(f.x.context, l), lane_of(f.x.tokens, l), 0, lane_of(f.x.q0, l)},
-              lane_of(f.tiles, l), lane_of(f.steps, l), lane_of(f.tile0, l), lane_of(f.step0, l)};
+              lane_of(f.tiles, l), lane_of(f.steps, l), (uint32_t)lane_of((int32_t)f.tile0, l), lane_of(f.step0, l)};
     }
     if (r0 + 64 >= reqs) return {};
   }
@@ -344,7 +347,8 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   // the tiles of rows, and the steps of each, that this workgroup computes
   Rows x;
   Shares all;
-  int32_t tiles = 0, steps = 1, tile0 = 0, from = 0, to = 1;  // steps [from, to) of tile x.tile
+  int32_t tiles = 0, steps = 1, from = 0, to = 1;  // steps [from, to) of tile x.tile
+  uint32_t tile0 = 0;
   int64_t left = 1;                                           // steps of this share, with those
   if constexpr (SHARED) {
     const Requests q = locate<ROWS, BN>(a, group, cap, lane, sp.shares, &all, [&](const Shares& s, const Requests& q) {
@@ -374,7 +378,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   for (;;) {
   const AttendArgs a = argument<AttendArgs>();
   if constexpr (SHARED) {
-    if (tile0 + x.tile >= sp.tiles) break;  // offsets that are not a CSR: the workspace has no slots for more
+    if (tile0 + x.tile >= (uint32_t)sp.tiles) break;  // offsets that are not a CSR: the workspace has no slots for more
     to = from + left < steps ? (int)(from + left) : steps;
   }
   const int row0 = x.tile * ROWS, rows = x.tokens * group;
@@ -704,7 +708,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   const bool whole = !SHARED || (from == 0 && to == steps);
   const float inv = l == 0 ? 0.0f : 1.0f / l;
   // where a part's row goes: share index of tile tile0 + x.tile
-  const int64_t part = ((int64_t)(index + tile0 + x.tile) * end.cache.num_kv_heads + g) * ROWS + (row - row0);
+  const int64_t part = ((int64_t)(index + (int32_t)(tile0 + x.tile)) * end.cache.num_kv_heads + g) * ROWS + (row - row0);
   constexpr int QUADS = KEYS ? 1 : 4;  // register quads of each 32 dimensions that this lane stores
 #pragma unroll
   for (int d = 0; d < DT; ++d)
@@ -764,14 +768,14 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, Split sp) {
   const int g = blockIdx.x % a.cache.num_kv_heads, tile = blockIdx.x / a.cache.num_kv_heads;
   Shares all;
   const Requests q = locate<ROWS, BN>(a, group, cap, lane, sp.shares, &all, [&](const Shares&, const Requests& q) {
-    return q.tile0 <= tile && tile < q.tile0 + q.tiles;
+    return tile - q.tile0 < (uint32_t)q.tiles;
   });
   if (q.steps == 0) return;  // no such tile
-  const int64_t begin = q.step0 + (int64_t)(tile - q.tile0) * q.steps;
+  const int64_t begin = q.step0 + (int64_t)(int32_t)(tile - q.tile0) * q.steps;
   const int s_from = share_of(all, begin), s_to = share_of(all, begin + q.steps - 1) + 1;
   if (s_to - s_from == 1) return;  // one share computed it whole
   Rows x = q.x;
-  x.tile = tile - q.tile0;
+  x.tile = (int32_t)(tile - q.tile0);
   const int rows = x.tokens * group - x.tile * ROWS, items = (rows < ROWS ? rows : ROWS) * quads;
   const int ways_log = s_to - s_from <= 8 ? 0 : s_to - s_from <= 16 ? 1 : 3;
   const int ways = 1 << ways_log, per = 256 >> ways_log, way = tid >> (8 - ways_log);
