@@ -300,7 +300,7 @@ struct Split {
 template <class E, int DP, bool KEYS, bool BY_BLOCK, bool SHARED>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendArgs args, BlockDiv div, Split sp) {
   const AttendArgs a = argument<AttendArgs>();
-  constexpr int ROWS = KEYS ? 32 : 128, BN = KEYS ? 128 : 64, KW = BN / 4;
+  constexpr int ROWS = KEYS ? kRowsKeys : kRows, BN = KEYS ? 128 : 64, KW = BN / 4;
   constexpr int VPR = DP / 8, RPI = 64 / VPR, NI = KW / RPI;
   constexpr int KT = KEYS ? 1 : 2, KSTEPS = DP / 16, DT = DP / 32;
   constexpr int KROW = DP * 2 + 16, VROW = DP * 2 + 64;  // bytes of a row in LDS
@@ -864,11 +864,11 @@ void launch_attend(const AttendArgs& a, BlockDiv div, const Split& sp, bool keys
   const dim3 join((unsigned)blocks, (unsigned)several);
   if (keys) {
     attend_kernel<E, DP, true, false, true><<<grid, 256, 0, stream>>>(a, div, sp);
-    join_kernel<E, 32, 128><<<join, 256, 0, stream>>>(a, sp);
+    join_kernel<E, kRowsKeys, 128><<<join, 256, 0, stream>>>(a, sp);
   } else {
     if (by_block) attend_kernel<E, DP, false, true, true><<<grid, 256, 0, stream>>>(a, div, sp);
     else attend_kernel<E, DP, false, false, true><<<grid, 256, 0, stream>>>(a, div, sp);
-    join_kernel<E, 128, 64><<<join, 256, 0, stream>>>(a, sp);
+    join_kernel<E, kRows, 64><<<join, 256, 0, stream>>>(a, sp);
   }
 }
 
@@ -1421,7 +1421,7 @@ hipError_t launch_attention(const AttendArgs& a, hipStream_t stream) {
   Split sp = {shares_within(p, a.cache, a.workspace_bytes), p.tiles, nullptr, nullptr};
   if (sp.shares > 0) {
     sp.acc = (float*)a.workspace;  // first: rows of 16-byte vectors
-    sp.lse = sp.acc + (int64_t)(sp.shares + p.tiles) * a.cache.num_kv_heads * (p.keys ? 32 : 128) * a.cache.head_dim;
+    sp.lse = sp.acc + (int64_t)(sp.shares + p.tiles) * a.cache.num_kv_heads * (p.keys ? kRowsKeys : kRows) * a.cache.head_dim;
   }
   const BlockDiv div = block_div(a.cache.block_size);
   if (a.cache.dtype == KVX_DTYPE_BF16) launch_attend_dims<Bf16>(a, div, sp, p.keys, stream);

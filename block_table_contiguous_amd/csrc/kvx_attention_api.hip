@@ -7,10 +7,12 @@
 
 #include "kvx_attention.h"
 #include "kvx_attention_launch.h"
+#include "kvx_attention_plan.h"
 
 namespace {
 
 constexpr int64_t kInt32Max = 0x7fffffff;
+constexpr int64_t kMaxRows = kInt32Max - 65536;  // query rows times heads: the rows of a few tiles past the last are counted too
 constexpr int64_t kMaxGroups = (1 << 22) - 1;  // workgroups along a grid dimension, up to 1024 threads each
 
 inline kvx_status from_hip(hipError_t e) { return e == hipSuccess ? KVX_SUCCESS : KVX_ERR_HIP; }
@@ -54,9 +56,17 @@ kvx_status check_batch(const kvx_paged_cache* c, const kvx_batch* b, int32_t num
   if (!b || b->num_reqs < 0 || b->num_reqs > 65535 || b->num_tokens < 0 || b->max_query_len < 0 ||
       b->max_context_len < 0 || num_heads < 1 || num_heads % c->num_kv_heads != 0 ||
       !table_ok(b->num_reqs, b->max_blocks_per_req, b->bt_row_stride, c->block_size) ||
-      b->num_tokens > kInt32Max / num_heads || (int64_t)b->num_reqs * c->num_kv_heads > kMaxGroups)
+      b->num_tokens > kMaxRows / num_heads || (int64_t)b->num_reqs * c->num_kv_heads > kMaxGroups)
     return KVX_ERR_INVALID_ARGUMENT;
   return st;
+}
+
+// check_batch for attention, which launches a workgroup a tile of rows.
+kvx_status check_attention(const kvx_paged_cache* c, const kvx_batch* b, int32_t num_heads) {
+  const kvx_status st = check_batch(c, b, num_heads);
+  if (st == KVX_ERR_INVALID_ARGUMENT) return st;
+  const int64_t rows = b->num_tokens * num_heads, least = kvx::kRows * (int64_t)b->num_reqs * c->num_kv_heads;
+  return rows <= kMaxRows - least ? st : KVX_ERR_INVALID_ARGUMENT;
 }
 
 bool batch_pointers(const kvx_paged_cache* c, const kvx_batch* b) {
@@ -124,7 +134,7 @@ kvx_status kvx_rope_and_cache(const kvx_paged_cache* cache, const void* query,
 
 int64_t kvx_paged_attention_workspace(const kvx_paged_cache* cache, const kvx_batch* batch,
                                       int32_t num_heads) {
-  if (check_batch(cache, batch, num_heads) != KVX_SUCCESS) return -1;
+  if (check_attention(cache, batch, num_heads) != KVX_SUCCESS) return -1;
   if (batch->num_reqs == 0 || batch->num_tokens == 0) return 0;
   return kvx::attention_workspace(*cache, *batch, num_heads);
 }
@@ -136,7 +146,7 @@ kvx_status kvx_paged_attention(const kvx_paged_cache* cache, const kvx_batch* ba
                                int64_t out_token_stride_bytes, int64_t out_head_stride_bytes,
                                float* lse, void* workspace, int64_t workspace_bytes,
                                int32_t* err_flag, hipStream_t stream) {
-  kvx_status st = check_batch(cache, batch, num_heads);
+  kvx_status st = check_attention(cache, batch, num_heads);
   if (st == KVX_ERR_INVALID_ARGUMENT) return st;
   if (!std::isfinite(scale) || !(scale > 0) || window < 0 || workspace_bytes < 0) return KVX_ERR_INVALID_ARGUMENT;
   for (kvx_status s : {check_rows(batch->num_tokens, num_heads, query_token_stride_bytes, query_head_stride_bytes),

@@ -12,6 +12,8 @@ namespace kvx {
 // batch's uneven contexts to a few rounds of workgroups, they are shared out evenly to kFill
 // workgroups, of kMinSteps steps at least, if there is a workspace for the parts.
 constexpr int kFill = 512, kMinSteps = 4;
+constexpr int64_t kRowsKeys = 32, kRows = 128;     // of a tile, by slots and otherwise
+constexpr int64_t kMaxWorkgroups = (1 << 24) - 1;  // of 256 threads: a launch has fewer than 2^32
 constexpr int64_t kMaxContext = 0x7fffffff;
 
 struct Plan {
@@ -23,8 +25,9 @@ inline Plan plan_attention(const kvx_paged_cache& c, const kvx_batch& b, int32_t
   const int64_t group = num_heads / c.num_kv_heads;
   const int64_t longest = b.max_query_len < b.num_tokens ? b.max_query_len : b.num_tokens;
   Plan p;
-  p.keys = longest * group <= 32;
-  const int64_t rows = p.keys ? 32 : 128, slots = p.keys ? 128 : 64;
+  // tiles of 32 rows also have to be few enough for a launch, as those of requests that keep to the hint are
+  p.keys = longest * group <= kRowsKeys && (b.num_tokens * group / kRowsKeys + b.num_reqs) * c.num_kv_heads <= kMaxWorkgroups;
+  const int64_t rows = p.keys ? kRowsKeys : kRows, slots = p.keys ? 128 : 64;
   p.tiles = (int32_t)(b.num_tokens * group / rows + b.num_reqs);
   int64_t busy = b.num_reqs * ((longest * group + rows - 1) / rows);
   if (busy > p.tiles) busy = p.tiles;
@@ -41,7 +44,7 @@ inline Plan plan_attention(const kvx_paged_cache& c, const kvx_batch& b, int32_t
 
 // Bytes of a slot: a part of one tile of every KV head.
 inline int64_t slot_bytes(const kvx_paged_cache& c, bool keys) {
-  return (int64_t)c.num_kv_heads * (keys ? 32 : 128) * 4 * ((int64_t)c.head_dim + 1);
+  return (int64_t)c.num_kv_heads * (keys ? kRowsKeys : kRows) * 4 * ((int64_t)c.head_dim + 1);
 }
 
 // The plan's shares in a workspace of so many bytes. One too small for the plan takes fewer, as long as they are more workgroups

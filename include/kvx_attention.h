@@ -138,8 +138,8 @@ kvx_status kvx_rope_and_cache(const kvx_paged_cache* cache, const void* query,
  * negative one, or a table entry outside the cache raises KVX_DEVERR_TABLE_RANGE or
  * KVX_DEVERR_BLOCK_RANGE and the slots concerned count as not seen; offsets that decrease or leave
  * [0, num_tokens] raise KVX_DEVERR_OFFSETS and are clamped.
- * Errors: INVALID_ARGUMENT (num_tokens*num_heads of 2^31 or more and max_blocks_per_req*block_size
- * above 2^31 - 65537 among them), MISALIGNED.
+ * Errors: INVALID_ARGUMENT (num_tokens*num_heads + 128*num_reqs*num_kv_heads above 2^31 - 65537, and
+ * max_blocks_per_req*block_size above that, among them), MISALIGNED.
  */
 kvx_status kvx_paged_attention(const kvx_paged_cache* cache, const kvx_batch* batch,
                                const void* query, int64_t query_token_stride_bytes,
@@ -164,7 +164,8 @@ int64_t kvx_paged_attention_workspace(const kvx_paged_cache* cache, const kvx_ba
  *   mass   float32 [num_reqs][num_kv_heads][mass_width] at the given strides (in floats, the last
  *          dimension dense); a context longer than mass_width raises KVX_DEVERR_TABLE_RANGE and
  *          is cut there. With mass_width or max_blocks_per_req 0 the call does nothing.
- * Only K is read. The last tokens of a prompt, or each decoded token in turn, are what callers
+ * Errors: INVALID_ARGUMENT (num_tokens*num_heads, or max_blocks_per_req*block_size, above 2^31 - 65537 among
+ * them), MISALIGNED. Only K is read. The last tokens of a prompt, or each decoded token in turn, are what callers
  * usually accumulate over.
  */
 kvx_status kvx_attention_mass(const kvx_paged_cache* cache, const kvx_batch* batch,

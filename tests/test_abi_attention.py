@@ -217,3 +217,25 @@ def test_binding_refuses_what_the_abi_cannot_see():
         a.update(kw)
         with pytest.raises(ValueError):
             K.kvx_rope_and_cache(**a)
+
+
+def test_row_counts_past_what_a_launch_can_number():
+    """Query rows near 2^31 are refused before anything is enqueued: the kernels count rows of a tile past the last one in
+    32 bits, and a launch has at most 2^32 threads."""
+    def size(c=None, H=4, **kw):
+        c = cache() if c is None else c
+        return K._F["kvx_paged_attention_workspace"](ctypes.byref(c), ctypes.byref(batch(**kw)), H)
+    one = cache(num_kv_heads=1)
+    top = (1 << 31) - 65537  # rows
+    for fn in (attend, mass):
+        assert fn(c=one, H=1, b=batch(num_tokens=top + 1)) == INVALID
+        assert fn(c=one, H=1, b=batch(num_tokens=(1 << 31) - 1)) == INVALID
+        assert fn(H=4, b=batch(num_tokens=top // 4 + 1)) == INVALID
+        # a count that is taken gets as far as the missing query
+        assert fn(c=one, H=1, b=batch(num_tokens=top - 3 * 128), q=None) == INVALID
+    assert size(c=one, H=1, num_tokens=top + 1) == -1 and size(c=one, H=1, num_tokens=top - 3 * 128) >= 0
+    # a request takes a tile of its own at least: 128 rows for every KV head of it
+    many = dict(num_reqs=65535, bt_row_stride=8)
+    assert size(c=cache(num_kv_heads=64), H=64, num_tokens=(top - 128 * 64 * 65535) // 64, **many) >= 0
+    assert size(c=cache(num_kv_heads=64), H=64, num_tokens=(top - 128 * 64 * 65535) // 64 + 2, **many) == -1
+    assert attend(c=cache(num_kv_heads=64), H=64, b=batch(num_tokens=(top - 128 * 64 * 65535) // 64 + 2, **many)) == INVALID

@@ -52,3 +52,16 @@ def test_one_long_request_is_split_as_far_as_the_workspace_goes(plans):
     batch = (1, 1, 1, 131072, 32, 8, 128)
     tiles = plans([(*batch, -1)])[0]["tiles"]
     assert [p["shares"] for p in plans([(*batch, -1 - tiles - k) for k in (1, 2, 5, 63, 64, 65)])] == [0, 2, 5, 63, 64, 64]
+
+
+def test_the_grid_stays_within_what_a_launch_can_have(plans):
+    """A tile is a workgroup of 256 threads for every KV head, and a launch has fewer than 2^32 threads, however long the
+    requests are that the hint calls short."""
+    top = (1 << 31) - 65537
+    for heads, kv, reqs in ((4, 2, 1), (1, 1, 1), (8, 8, 100), (64, 64, 65535), (32, 1, 65535)):
+        for rows in (1 << 29, 1 << 30, top - 128 * kv * reqs):
+            for hint in (0, 1, 2, 1 << 40):
+                p = plans([(reqs, rows // heads, hint, 64, heads, kv, 8, -1)])[0]
+                assert 0 < p["tiles"] * kv < 1 << 24, (heads, kv, reqs, rows, hint, p)
+    p = plans([(65535, 65535, 1, 8192, 64, 64, 128, -1)])[0]  # the largest true batch of single tokens keeps its kind
+    assert p["keys"] == 1
