@@ -179,7 +179,9 @@ __device__ __forceinline__ void loads_landed() {
 // masses, a tile of slots at a time: all its loads, then all its stores. An ascending list has
 // keep[i] >= i, so a slot is read in its own tile or an earlier one; with the tiles of a column in
 // one workgroup (grid.y = 1), in order and with a barrier between a tile's loads and its stores,
-// the move is right in place. Where source and destination differ, grid.y spreads the tiles.
+// the move is right in place. Where source and destination differ, grid.y spreads the tiles; a row whose destination
+// block is the source's own of that place (a copy of the table, or part of one) would then race with the reads of it, and
+// is left alone.
 __global__ __launch_bounds__(kMoveThreads) void compact_kernel(CompactArgs a, BlockDiv div) {
   const kvx_paged_cache& cache = a.cache;
   const int columns = 2 * cache.num_kv_heads + (a.mass ? a.num_heads : 0);
@@ -234,7 +236,7 @@ __global__ __launch_bounds__(kMoveThreads) void compact_kernel(CompactArgs a, Bl
     for (int64_t t0 = (int64_t)blockIdx.y * tile_rows; t0 < a.budget; t0 += (int64_t)gridDim.y * tile_rows) {
       // Three rounds of loads, each issued whole: list entries, table entries, rows. What is not to be
       // moved reads the first entry or row instead, and is not stored.
-      int32_t k[kMoveUnroll], sb[kMoveUnroll], db[kMoveUnroll];
+      int32_t k[kMoveUnroll], sb[kMoveUnroll], db[kMoveUnroll], own[kMoveUnroll];  // own: the source's block at d
       bool move[kMoveUnroll];
 #pragma unroll
       for (int u = 0; u < kMoveUnroll; ++u) {
@@ -249,16 +251,20 @@ __global__ __launch_bounds__(kMoveThreads) void compact_kernel(CompactArgs a, Bl
         const int32_t s = block_of(div, k[u]), d = block_of(div, i);
         if (move[u] && (s >= a.src_cols || d >= a.dst_cols)) errs |= KVX_DEVERR_TABLE_RANGE, move[u] = false;
         k[u] = move[u] ? k[u] - s * div.size : 0;  // places in the blocks from here on
-        piece[u] = (piece[u] & 0xffff) | (move[u] && in_place && s == d && k[u] == i - d * div.size ? 1 << 16 : 0);
+        piece[u] = (piece[u] & 0xffff) | (move[u] && s == d && k[u] == i - d * div.size ? 1 << 16 : 0);
         sb[u] = gload<int32_t>(from + (move[u] ? s : 0));
         db[u] = gload<int32_t>(to + (move[u] ? d : 0));
+        own[u] = in_place ? 0 : gload<int32_t>(from + (move[u] ? d : 0));  // d <= s
       }
       u32x4 v[kMoveUnroll];
 #pragma unroll
       for (int u = 0; u < kMoveUnroll; ++u) {
         if (move[u] && ((uint32_t)sb[u] >= (uint64_t)cache.num_blocks || (uint32_t)db[u] >= (uint64_t)cache.num_blocks))
           errs |= KVX_DEVERR_BLOCK_RANGE, move[u] = false;
-        move[u] = move[u] && !(piece[u] >> 16);
+        if (in_place || own[u] == db[u]) {  // one block on both sides: its row may be there already
+          if (move[u] && !in_place && !(piece[u] >> 16)) errs |= KVX_DEVERR_BLOCK_RANGE, move[u] = false;
+          move[u] = move[u] && !(piece[u] >> 16);
+        }
         const char* src = (const char*)cache.base + at + (piece[u] & 0xffff);
         if (move[u]) src += sb[u] * cache.block_stride_bytes + (int64_t)k[u] * cache.token_stride_bytes;
         v[u] = __builtin_nontemporal_load((const __attribute__((address_space(1))) u32x4*)src);

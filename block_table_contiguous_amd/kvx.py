@@ -840,7 +840,9 @@ def kvx_evict_select(mass, context_lens, budget: int, sink: int, recent: int, ke
 def kvx_evict_compact(kv_cache, block_table, dst_block_table, keep, mass=None, mass_out=None,
                       layout: str = "blocks_tokens_kv", err_flag=None, stream=None):
     """Move the kept slots' K and V rows (and masses) together, slot keep[r][h][i] to slot i of
-    dst_block_table: block_table itself for a move in place, else a table of other blocks."""
+    dst_block_table: block_table itself (the same tensor, whole) for a move in place, else a table of
+    blocks none of which is a source block. A copy of block_table is not in place: rows that would
+    move within it are skipped and raise DEVERR_BLOCK_RANGE."""
     import torch
 
     c = _cache(kv_cache, layout)

@@ -203,7 +203,10 @@ kvx_status kvx_evict_select(const float* mass, int64_t mass_req_stride, int64_t 
  *   dst_block_table  may be block_table itself (same pointer): the move is then in place, the
  *              blocks after the kept slots are free afterwards, and no block may belong to two
  *              requests. Otherwise the destination blocks must be none of the source blocks, and
- *              the sources keep their bytes (a shared prefix stays whole for its other owners).
+ *              the sources keep their bytes (a shared prefix stays whole for its other owners). A copy
+ *              of the source table is not "in place": a row that would go to the request's own
+ *              source block of that column is skipped and raises KVX_DEVERR_BLOCK_RANGE, unless it is
+ *              there already. Source blocks at other columns or of other requests are not looked for.
  *   keep       int32 [num_reqs][num_heads][budget], ascending, -1 after the last (as
  *              kvx_evict_select writes it); negative entries move nothing.
  *   mass, mass_out  float32 [num_reqs][num_heads][width] at the given strides, or both NULL:
