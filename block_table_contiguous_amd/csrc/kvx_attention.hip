@@ -297,6 +297,8 @@ struct Split {
 // K and V go from memory to registers one tile ahead and then to LDS, in rows padded so that the reads of
 // 16 rows (K: 16 bytes a row), or of 4 slots x 64 bytes (V: 64 bytes a row), fall on different banks;
 // padding, unlike a swizzle, leaves every address one register and a constant.
+// The shared variants do not fit their registers whole: at 128 dimensions 10 to 17 values a lane are in scratch (44-72 bytes), at 256
+// 70 to 84 (284-340 bytes), all of them what a tile's start and end use, none in the loop over the slots.
 template <class E, int DP, bool KEYS, bool BY_BLOCK, bool SHARED>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendArgs args, BlockDiv div, Split sp) {
   const AttendArgs a = argument<AttendArgs>();
@@ -1042,7 +1044,11 @@ __device__ __forceinline__ float row_sums(char* own, const f32x16 (&sum)[2], int
 // LDS. Every slot belongs to one wavefront, so nothing is joined between workgroups and the order of
 // the sum is fixed. The exponentials bound it, then the products.
 constexpr int kMassSlots = 256;  // of a workgroup
-constexpr int kMassFill = 4096;  // workgroups that fill the GPU with few rows
+// Workgroups that fill the GPU with few rows. A decode step's time hardly changes with their size between a launch too large (128
+// slots each) and too uneven (8192): 32 requests of up to 8192 slots, 8 KV heads, 101 us with 128 slots, 90 with the rule's 512,
+// 101 with 2048, 116 with 8192; 256 on one KV head 101, 83 (rule), 87, 102; one of 131072 58, 48 with the rule's 256, 46, 103. The
+// most, 4096 slots, keeps a batch too large for the rule from that end.
+constexpr int kMassFill = 4096;
 
 template <class E, int DP>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void mass_kernel(MassArgs ma, BlockDiv div) {
@@ -1452,6 +1458,11 @@ hipError_t launch_mass(const MassArgs& m, hipStream_t stream) {
     if (per < 128) per = 128;
     if (per > 4096) per = 4096;
   } else if ((slots + kMassSlots - 1) / kMassSlots * lists < (m.at.cache.head_dim <= 128 ? kFill : kFill / 3)) {
+    // Two workgroups a CU of mass_kernel, or one where the widest heads take the registers of two. Many rows, 512 tokens of 8 heads
+    // on one over 4096 slots: 64, 256 and 512 workgroups by slots 124, 130 and 174 us, by rows 32, 111 and 217; at 256
+    // dimensions 64, 128 and 256 of them 207, 206 and 209 against 70, 128 and 243. A prompt of 8192 tokens (32): 1522
+    // against 340, at 256 dimensions 2806 against 840. With few rows the two meet earlier (61 tokens of 4 heads a KV head: 128
+    // workgroups 14 against 12 us, 256 15 against 22, 384 17 against 32), at a loss of microseconds.
     how = kMassByRows;
     per = 64;
   }

@@ -2,12 +2,13 @@
 //
 // One workgroup a token. Its first rot_dim/2 threads form the angles' cosines and sines once for
 // all heads: position x inv_freq in 64 bits, reduced to a fraction of a turn there, because a
-// 32-bit product is off by whole radians at far positions (2^20 x 2^-24 x 2 pi and more); the
-// functions themselves then take the fraction in 32 bits. The rows are moved as 16-byte vectors,
+// 32-bit product is off by up to 1/16 of a radian at an angle of 2^20, by a whole one from 2^24 on and by 64 below 2^31;
+// the functions themselves then take the fraction in 32 bits. The rows are moved as 16-byte vectors,
 // a thread holding both halves of its pairs; each is read and written once, and that is the bound:
 // HBM bytes for many tokens, one launch and two dependent loads for a few. The first rows are on their
 // way while the angles are formed, and the next ones while a thread turns its own (9461
-// tokens of 32 + 8 heads of 128: 233 MB in 45 us). Stores go by the caches' default policy: the attention reads
+// tokens of 32 + 8 heads of 128: 233 MB in 45-47 us with the pairs half a rotation apart, 50 side by side, where a thread
+// has one vector in flight and not two; 49-56 where only 64 or 16 of the dimensions turn). Stores go by the caches' default policy: the attention reads
 // the rows next.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -134,6 +134,8 @@ kvx_status kvx_rope_and_cache(const kvx_paged_cache* cache, const void* query,
  *                or, where that would leave the GPU idle, not at all.
  *                Calls that may run at the same time, replayed graphs among them, need one each.
  *   scale        finite and > 0.
+ *   window       counts slots, not positions: after an eviction the last `window` tokens that were kept. With
+ *                causal == 0 every row of a request sees the same last `window` slots of its context.
  * Rows that belong to nobody are left as they were. A context longer than the block table's row, a
  * negative one, or a table entry outside the cache raises KVX_DEVERR_TABLE_RANGE or
  * KVX_DEVERR_BLOCK_RANGE and the slots concerned count as not seen; offsets that decrease or leave
