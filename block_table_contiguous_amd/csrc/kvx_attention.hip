@@ -230,6 +230,18 @@ template <class E>
 constexpr float kLift = __is_same(E, Fp16) ? 11.0f : 0.0f;
 template <class E>
 constexpr float kLag = __is_same(E, Fp16) ? 4.0f : 8.0f;
+// Scores of 2^20 and more, in base 2, are far: 32 bits hold them in steps of 2^-3, and from 2^24 on the rounding of x alone decides
+// over the weight's exponent. x is then rounded before the reference is taken from it, as the maximum was, so that the largest
+// weight is what the reference says; in one step, unrounded, it could end anywhere up to half a step of x.
+__device__ __forceinline__ bool is_far(float x) { return __builtin_amdgcn_frexp_expf(x) > 20; }  // not of an infinity
+__device__ __forceinline__ float rounded_product(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
+}
+__device__ __forceinline__ float rounded_difference(float a, float b) {
+#pragma clang fp contract(off)
+  return a - b;
+}
 
 template <class E>
 __device__ __forceinline__ bool non_finite(u32x4 v) {
@@ -256,6 +268,11 @@ __device__ __forceinline__ int here(int x) {
   asm volatile("" : "+v"(x));
   return x;
 }
+__device__ __forceinline__ float here(float x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+__device__ __forceinline__ int lane_here() { return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, here(0))); }
 
 // A buffer that starts at p (the same in all lanes) for loads whose offsets the caller keeps inside
 // the memory: a scalar base, a scalar step and a lane's constant offset make an address for nothing.
@@ -335,6 +352,11 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
   const int kw = KEYS ? w * KW : 0;  // first slot of a tile that this wavefront computes
   const char* const sk_get = sk + (kw + n) * KROW + hf * 16;
   const char* const sv_get = sv + (kw + 4 * hf + ((lane & 15) >> 2)) * VROW + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+  // This lane's place for the reference of its row: in the padding of the V rows that it stages.
+  auto reference = [&]() -> float* {
+    const int piece = lane_here() % VPR;
+    return (float*)(sv_put - 16 * piece + DP * 2 + 4 * piece + (piece >= 16 ? RPI * VROW - 64 : 0));
+  };
   auto clear_padding = [&]() {
     if (vecs < VPR && c >= vecs) {
 #pragma unroll
@@ -431,6 +453,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
 #pragma unroll
   for (int d = 0; d < DT; ++d) acc[d] = f32x16{};
   float m = -INFINITY, l = 0;
+  *reference() = m;
   const float c1 = a.scale * kLog2e;
 
   // Staging. BY_BLOCK, where 16 slots always lie in one block: their rows are token_stride apart, and the block
@@ -555,7 +578,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
       for (int kt = 0; kt < KT; ++kt)  // no product waits for the one before it
         s[kt] = mfma(E(), *(const u32x4*)(sk_get + kt * 32 * KROW + st * 32),
                      Q_LDS ? *(const u32x4*)(sq + st * 32) : q[Q_LDS ? 0 : st], s[kt]);
-    // K is read eight pieces ahead of the products: read as they are needed, each would wait for LDS
+    // K is read eight pieces ahead of the products: read as they are needed, each would wait for LDS. The compiler keeps to
+    // this order in the unshared variants at 128 dimensions (rows: by block) and in part at 64 and 256, but not in the shared ones,
+    // whose registers are full.
     if constexpr (!Q_LDS) {
     __builtin_amdgcn_sched_group_barrier(kDsRead, 8, 0);
 #pragma unroll
@@ -583,16 +608,29 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kt][i]);
     top = fmaxf(top, other_half(top)) * c1;
-    // The reference moves only when the maximum leaves its range: the sums keep their 32 bits.
+    // The reference moves only when the maximum leaves its range: the sums keep their 32 bits. What only this needs is kept
+    // in LDS or formed here: with a register more in the loop the compiler no longer reads K ahead of the products above
+    // (1042 -> 1150 us at 2048 queries of 32 heads over 32768 slots).
     if (__any(top > m + (kLift<E> + kLag<E>))) {
-      const float to = top > m + (kLift<E> + kLag<E>) ? top - kLift<E> : m;
-      const float shrink = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-      m = to;
+      float* const mine = reference();
+      const float held = *mine, now = here(top);
+      const float to = now - held > kLift<E> + kLag<E> ? (is_far(now) ? now : now - kLift<E>) : held;
+      const float shrink = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(held - to);
+      *mine = m = to;
       l *= shrink;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[d][i] *= shrink;
+      if (__any(is_far(to))) {
+        // the scores become what they stand above the reference, and m is such that the next tile comes here again
+        const float from = to == -INFINITY ? 0.0f : to, factor = here(c1), back = 1.0f / factor;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[kt][i] = rounded_difference(rounded_product(s[kt][i], factor), from) * back;
+        m = -INFINITY;
+      }
     }
     const float ref = m == -INFINITY ? 0.0f : m;
     // Weights and products by 16 slots: V is read one group ahead, and the weights of a group are
@@ -661,6 +699,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(AttendAr
     else lds_barrier();
   }
   l += other_half(l);
+  m = *reference();
 
   if constexpr (KEYS) {
     // join the wavefronts: weights of each one's sum, then the sums themselves through LDS
