@@ -1,5 +1,5 @@
-"""Build libkvx.so (the HIP library behind the C ABI in include/kvx.h and include/kvx_attention.h)
-for gfx950, in-tree.
+"""Build libkvx.so (the HIP library behind the C ABI in include/kvx.h, include/kvx_attention.h and
+include/kvx_fp4.h) for gfx950, in-tree.
 
     python -m block_table_contiguous_amd.build          # compile
     python -m block_table_contiguous_amd.build --asm    # also keep the device assembly
@@ -21,6 +21,8 @@ LIB = os.path.join(PKG, "libkvx.so")
 SOURCES = ["kvx_api.hip", "kvx_kernels.hip", "kvx_signal.hip"]  # the transfer path (include/kvx.h)
 # the calls that compute on a paged cache (include/kvx_attention.h)
 ATTENTION_SOURCES = ["kvx_attention_api.hip", "kvx_attention.hip", "kvx_rope.hip", "kvx_evict.hip"]
+# the same on a cache held in 4 bits (include/kvx_fp4.h)
+FP4_SOURCES = ["kvx_fp4_api.hip", "kvx_fp4_attention.hip", "kvx_fp4_cache.hip"]
 ARCH = "gfx950"
 
 # Packed-FP32 instructions are disabled for all device code: the copy kernels do no float
@@ -45,7 +47,7 @@ def build(asm_dir: str | None = None, verbose: bool = False) -> str:
     objs = []
     tmp = os.path.join(PKG, "_build")
     os.makedirs(tmp, exist_ok=True)
-    sources = SOURCES + ATTENTION_SOURCES
+    sources = SOURCES + ATTENTION_SOURCES + FP4_SOURCES
     jobs = []
     for src in sources:  # one compiler process a source, at once
         obj = os.path.join(tmp, src.replace(".hip", ".o"))

@@ -1,0 +1,487 @@
+// gfx950 kernels of kvx_paged_attention_fp4.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kvx_attention_rows.h"
+#include "kvx_fp4_format.h"
+#include "kvx_fp4_launch.h"
+#include "kvx_fp4_plan.h"
+
+namespace kvx {
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+// --------------------------------------------------------------------------------------
+// matrix pieces
+// --------------------------------------------------------------------------------------
+
+// 16x16x32: lane l = 16 g + n holds row (or column) n and elements 8 g to 8 g + 7 of the summed dimension; result register i of
+// lane l is row 4 g + i, column n. Products of 4-bit K with q split into 8-bit floats (the scaled products' types) would spare K's
+// conversion, but they cut off what is 2^-11 of the largest of the products they add at once, which a sum of weights shows.
+__device__ __forceinline__ f32x4 product(Bf16, u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(Bf16::V8, a), __builtin_bit_cast(Bf16::V8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 product(Fp16, u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(Fp16::V8, a), __builtin_bit_cast(Fp16::V8, b), c, 0, 0, 0);
+}
+
+// Largest and sum over the lanes l, l ^ 16, l ^ 32, l ^ 48.
+template <class F>
+__device__ __forceinline__ float over_rows(float x, F f) {
+  uint32_t b = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  const uint32_t r0 = r[0], r1 = r[1];
+  x = f(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
+  b = __builtin_bit_cast(uint32_t, x);
+  const auto s = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  const uint32_t s0 = s[0], s1 = s[1];
+  return f(__builtin_bit_cast(float, s0), __builtin_bit_cast(float, s1));
+}
+__device__ __forceinline__ float max_over_rows(float x) {
+  return over_rows(x, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float sum_over_rows(float x) {
+  return over_rows(x, [](float a, float b) { return a + b; });
+}
+
+// Where v may read back infinite or NaN in the type.
+template <class E>
+constexpr uint32_t kFiniteScales = __is_same(E, Bf16) ? 252 : 140;
+
+// One code in the type, widened.
+template <class E>
+__device__ __forceinline__ f32x4 decode4(uint32_t codes, float scale) {
+  const u32x4 r = decode<E>(codes, scale);
+  const u32x2 two = {r[0], r[1]};
+  return __builtin_convertvector(__builtin_bit_cast(typename E::V4, two), f32x4);
+}
+
+// --------------------------------------------------------------------------------------
+// attention
+// --------------------------------------------------------------------------------------
+
+// One pass over the slots with a running maximum and sum, scores transposed (S^T = K q^T), so that a lane holds one query
+// row and four slots of each 16, and the weights are where O^T += V^T P^T takes them. RT tiles of 16 rows are the same for the
+// four wavefronts of a workgroup, which take 32 slots each of every 128 and meet only at the end. A lane loads whole groups of 32
+// elements with their scales. Of K, widened to 16 bits, they are the matrix unit's operand as they stand, because the summed dimension
+// may be numbered in any order; V goes widened to LDS and is read from there with the transposing load. DP is head_dim padded to 64, 128 or 256.
+//   SHARED: the grid's workgroups take equal shares of the whole batch's steps (see Shares).
+template <class E, int DP, int RT, bool SHARED>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(AttendArgs args, BlockDiv div, Split sp) {
+  const AttendArgs a = argument<AttendArgs>();
+  constexpr int ROWS = 16 * RT, KW = 32, BN = 4 * KW, KT = KW / 16;
+  constexpr int KS = DP > 128 ? 2 : 1, DT = DP / 16;
+  constexpr int VROW = DP * 2 + 32;  // bytes of a row of V in LDS
+  constexpr int TILE = 4 * KW * VROW, JOIN = 4 * 16 * DP * 4;
+  __shared__ __align__(16) char smem[TILE > JOIN ? TILE : JOIN];
+  __shared__ float sm[2][4][ROWS];
+
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform((int32_t)(tid >> 6));
+  const int n = lane & 15, hq = lane >> 4;
+  const int group = a.num_heads / a.cache.num_kv_heads, dim = a.cache.head_dim, groups = dim / kGroup;
+  const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size;
+  int g = blockIdx.x % a.cache.num_kv_heads, index = blockIdx.x / a.cache.num_kv_heads;
+  if constexpr (SHARED) {  // shares that follow one another to one XCD: workgroup i runs on XCD i % 8
+    const int xcd = blockIdx.x % 8, per = gridDim.x / 8, more = gridDim.x % 8;
+    const int at = xcd * per + (xcd < more ? xcd : more) + blockIdx.x / 8;
+    g = at / sp.shares;
+    index = at - g * sp.shares;
+  }
+  if (blockIdx.x == 0) check_batch(a, cap, tid, 256);
+
+  char* const own = smem + w * KW * VROW;  // this wavefront's rows of V
+  char* const put = own + n * VROW + hq * 64;
+  const char* const get = own + (4 * hq + (n >> 2)) * VROW + (n & 3) * 8;
+
+  Rows x;
+  Shares all;
+  int32_t tiles = 0, steps = 1, from = 0, to = 1;  // steps [from, to) of tile x.tile
+  uint32_t tile0 = 0;
+  int64_t left = 1;
+  if constexpr (SHARED) {
+    const Requests q = locate<ROWS, BN>(a, group, cap, lane, sp.shares, &all, [&](const Shares& s, const Requests& q) {
+      const int64_t begin = share_begin(s, index);
+      return index < s.count && q.step0 <= begin && begin < q.step0 + (int64_t)q.tiles * q.steps;
+    });
+    if (q.steps == 0) return;
+    const int64_t begin = share_begin(all, index);
+    left = share_begin(all, index + 1) - begin;
+    tile0 = q.tile0;
+    tiles = q.tiles;
+    steps = q.steps;
+    x = q.x;
+    x.tile = (int32_t)quotient(begin - q.step0, steps);
+    from = (int32_t)(begin - q.step0 - (int64_t)x.tile * steps);
+  } else {
+    x = find_rows<ROWS>(a, sp.tiles - 1 - index, group, cap, lane);
+    if (x.tile < 0 || (int64_t)x.tile * ROWS >= (int64_t)x.tokens * group) return;
+  }
+  int errs = 0;
+  for (;;) {
+  if constexpr (SHARED) {
+    if (tile0 + x.tile >= (uint32_t)sp.tiles) break;  // offsets that are not a CSR: the workspace has no slots for more
+    to = from + left < steps ? (int)(from + left) : steps;
+  }
+  const int row0 = x.tile * ROWS, rows = x.tokens * group;
+
+  // this lane's rows, what they see, and what any row of the workgroup sees
+  int2 see[RT];
+  int head[RT];
+  int64_t q_row[RT];
+  bool used[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int row = row0 + rt * 16 + n;
+    used[rt] = row < rows;
+    const int token = used[rt] ? row / group : 0;
+    head[rt] = g * group + (used[rt] ? row - token * group : 0);
+    q_row[rt] = x.q0 + token;
+    see[rt] = sees(a, x, token);
+    if (!used[rt]) see[rt] = {0, 0};
+  }
+  const int last_row = row0 + ROWS < rows ? row0 + ROWS - 1 : rows - 1;
+  const int2 first = sees_uniform(a, x, row0 / group), last = sees_uniform(a, x, last_row / group);
+  const int kend = last.y;
+  const int t_first = first.x / BN, t_all = (kend + BN - 1) / BN - t_first;
+  int tb = t_first, te = t_first + (t_all > 0 ? t_all : 0);
+  if constexpr (SHARED) {
+    if (t_all == steps) {
+      tb = t_first + from;
+      te = t_first + to;
+    } else {  // a tile whose rows see less than all of the request's: its steps in proportion
+      const int64_t mine = te - tb;
+      te = tb + (int)quotient(mine * to, steps);
+      tb = tb + (int)quotient(mine * from, steps);
+    }
+  }
+  tb = uniform(tb);
+  te = uniform(te);
+
+  // q: lane 16 g + n has group g (and g + 4) of row n, as it will have of K
+  u32x4 q[RT][KS][4];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const char* p = a.query.base + q_row[rt] * a.query.token_stride + head[rt] * a.query.head_stride;
+#pragma unroll
+    for (int c = 0; c < KS; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        q[rt][c][k] = u32x4{0, 0, 0, 0};
+        if (used[rt] && c * 4 + hq < groups) q[rt][c][k] = gload<u32x4>(p + (c * 4 + hq) * (kGroup * 2) + k * 16);
+      }
+  }
+
+  const char* const base = (const char*)a.cache.base + g * a.cache.head_stride_bytes;
+  const int64_t scales = (int64_t)a.cache.block_size * (dim / 2);
+  const int32_t* const table = a.batch.block_table + x.r * a.batch.bt_row_stride;
+  const int cols = (int)a.batch.max_blocks_per_req;
+
+  f32x4 acc[RT][DT];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    m[rt] = -INFINITY;
+    l[rt] = 0;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) acc[rt][d] = f32x4{};
+  }
+  const float c1 = a.scale * kLog2e;
+
+  // Lane 16 g + n of a wavefront stages group g (and g + 4) of slots n and 16 + n of its 32. A slot that is not there is read
+  // from the cache's first rows; its scale of V becomes 0 and its weight is.
+  int32_t ids[KT];
+  auto load_ids = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+      const int b = block_of(div, t * BN + w * KW + i * 16 + n);
+      ids[i] = gload<int32_t>(table + (b < cols ? b : cols - 1));
+    }
+  };
+  u32x4 rk[KT][KS], rv[KT][KS];
+  uint32_t ks[KT][KS], vs[KT][KS];
+  uint32_t there = 0;
+  auto fetch = [&](int t) {
+    there = 0;
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+      const int j = t * BN + w * KW + i * 16 + n;
+      const bool in = j < kend, ok = in && (uint32_t)ids[i] < (uint64_t)a.cache.num_blocks;
+      if (in && !ok) errs |= KVX_DEVERR_BLOCK_RANGE;
+      there |= (uint32_t)(__ballot(ok) & 0xffff) << (16 * i);
+      const int o = j - block_of(div, j) * div.size;
+      const char* k = base + (ok ? ids[i] * a.cache.block_stride_bytes : 0);
+      const char* e = k + (ok ? o : 0) * (dim / 2);
+      const char* s = k + scales + (ok ? o : 0) * groups;
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        const int at = c * 4 + hq;
+        rk[i][c] = rv[i][c] = u32x4{0, 0, 0, 0};
+        ks[i][c] = vs[i][c] = 0;
+        if (at < groups) {
+          rk[i][c] = gload<u32x4>(e + at * 16);
+          ks[i][c] = gload<uint8_t>(s + at);
+          rv[i][c] = gload<u32x4>(e + at * 16 + a.cache.kv_stride_bytes);
+          vs[i][c] = gload<uint8_t>(s + at + a.cache.kv_stride_bytes);
+        }
+      }
+    }
+  };
+
+  if (tb < te) {
+    load_ids(tb);
+    fetch(tb);
+    load_ids(tb + 1);
+  }
+  for (int t = tb; t < te; ++t) {
+    const int k0 = t * BN + w * KW;
+    const bool inner = t * BN >= last.x && t * BN + BN <= first.y;
+    const uint32_t here_mask = there;
+    f32x4 s[RT][KT];
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) s[rt][i] = f32x4{};
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        const float scale = scale_of(ks[i][c]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const u32x4 wide = decode<E>(rk[i][c][k], scale);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) s[rt][i] = product(E(), wide, q[rt][c][k], s[rt][i]);
+        }
+      }
+    }
+    // A weight of zero times a NaN or infinity is NaN: groups of V that may read back as one are left out of the products
+    // and added below for the rows that see them.
+    uint64_t odd[KT][KS], any_odd = 0;
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        odd[i][c] = 0;
+        if (!(here_mask >> (16 * i + n) & 1)) vs[i][c] = 0;
+        if (!inner) {
+          const bool bad = vs[i][c] > kFiniteScales<E>;
+          any_odd |= odd[i][c] = __ballot(bad);
+          if (bad) vs[i][c] = 0, rv[i][c] = u32x4{0, 0, 0, 0};
+        }
+        const float scale = scale_of(vs[i][c]);
+        char* at = put + i * 16 * VROW + c * 256;
+        if (DP >= 128 || hq * 32 < DP) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) *(u32x4*)(at + k * 16) = decode<E>(rv[i][c][k], scale);
+        }
+      }
+    __builtin_amdgcn_wave_barrier();
+    if (t + 1 < te) {
+      fetch(t + 1);
+      load_ids(t + 2);
+    }
+
+    u32x4 p[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      if (!inner || here_mask != 0xffffffffu) {
+        const int at = k0 + 4 * hq, lo = see[rt].x - at, hi = see[rt].y - at;
+        const uint32_t mine = here_mask >> (4 * hq);
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int o = 16 * i + r;
+            if (o < lo || o >= hi || !(mine >> o & 1)) s[rt][i][r] = -INFINITY;
+          }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top = fmaxf(top, s[rt][i][r]);
+      top = max_over_rows(top) * c1;
+      // the reference moves only when the maximum leaves its range: the sums keep their 32 bits
+      bool far = false;
+      if (__any(top > m[rt] + (kLift<E> + kLag<E>))) {
+        const float held = m[rt];
+        const float to = top - held > kLift<E> + kLag<E> ? (is_far(top) ? top : top - kLift<E>) : held;
+        const float shrink = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(held - to);
+        m[rt] = to;
+        l[rt] *= shrink;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) acc[rt][d] *= shrink;
+      }
+      far = __any(is_far(m[rt]));
+      const float ref = m[rt] == -INFINITY ? 0.0f : m[rt];
+      f32x8 pv;
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float v = s[rt][i][r];
+          // far: rounded before the reference is taken from it, as the maximum was
+          const float e = far ? rounded_difference(rounded_product(v, c1), ref) : __builtin_fmaf(v, c1, -ref);
+          l[rt] += pv[4 * i + r] = __builtin_amdgcn_exp2f(e);
+          s[rt][i][r] = pv[4 * i + r];
+        }
+      p[rt] = narrow<E>(pv);  // one rounding of each weight to the element type, which the matrix unit takes
+    }
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      const char* at = get + d * 32;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KVX_LDS s16x4*)at);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KVX_LDS s16x4*)(at + 16 * VROW));
+      const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) acc[rt][d] = product(E(), __builtin_bit_cast(u32x4, v), p[rt], acc[rt][d]);
+    }
+    if (any_odd) {
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int c = 0; c < KS; ++c)
+          for (uint64_t todo = odd[i][c]; todo; todo &= todo - 1) {
+            const int from = __builtin_ctzll(todo), o = from & 15, at = c * 4 + (from >> 4), j = k0 + i * 16 + o;
+            const int b = block_of(div, j);
+            const char* plane = base + table[b] * a.cache.block_stride_bytes + a.cache.kv_stride_bytes;
+            const int in = j - b * div.size;
+            const float scale = scale_of(gload<uint8_t>(plane + scales + in * groups + at));
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              const float mine = o % 4 == 0 ? s[rt][i][0] : o % 4 == 1 ? s[rt][i][1] : o % 4 == 2 ? s[rt][i][2] : s[rt][i][3];
+              const float pj = __shfl(mine, n + 16 * (o >> 2));
+              if (j < see[rt].x || j >= see[rt].y) continue;
+#pragma unroll
+              for (int d = 0; d < DT; ++d) {
+                if (d >> 1 != at) continue;
+                const uint32_t codes = gload<uint16_t>(plane + in * (dim / 2) + d * 8 + 2 * hq);
+                acc[rt][d] += pj * decode4<E>(codes, scale);
+              }
+            }
+          }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+
+  // join the wavefronts: weights of each one's sum, then the sums themselves through LDS
+  const AttendArgs end = argument<AttendArgs>();
+  const bool whole = !SHARED || (from == 0 && to == steps);
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    l[rt] = sum_over_rows(l[rt]);
+    if (hq == 0) {
+      sm[0][w][rt * 16 + n] = m[rt];
+      sm[1][w][rt * 16 + n] = l[rt];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    float top = -INFINITY, total = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, sm[0][i][rt * 16 + n]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) total += sm[1][i][rt * 16 + n] * __builtin_amdgcn_exp2f(sm[0][i][rt * 16 + n] - ref);
+    const float mine = __builtin_amdgcn_exp2f(m[rt] - ref);
+    // [wavefront][row][16-byte pieces, swizzled by row]
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+      *(f32x4*)(smem + ((w * 16 + n) * (DP / 4) + ((d * 4 + hq) ^ n)) * 16) = acc[rt][d] * mine;
+    __syncthreads();
+    const float inv = total == 0 ? 0.0f : 1.0f / total;
+    // where a part's row goes: share index of tile tile0 + x.tile
+    const int64_t part = ((int64_t)(index + (int32_t)(tile0 + x.tile)) * end.cache.num_kv_heads + g) * ROWS + rt * 16 + n;
+#pragma unroll
+    for (int i = 0; i < DT / 4; ++i) {
+      const int d = i * 4 + w, e = d * 16 + 4 * hq;
+      f32x4 v = {};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v += *(const f32x4*)(smem + ((k * 16 + n) * (DP / 4) + ((d * 4 + hq) ^ n)) * 16);
+      v = total == 0 ? f32x4{} : v * inv;
+      if (!used[rt] || e >= end.cache.head_dim) continue;
+      if (SHARED && !whole) {
+        gstore(sp.acc + part * end.cache.head_dim + e, v);
+      } else {
+        gstore((char*)end.out.base + q_row[rt] * end.out.token_stride + head[rt] * end.out.head_stride + e * 2,
+               __builtin_convertvector(v, typename E::V4));
+      }
+    }
+    if (used[rt] && hq == 0 && w == 0) {
+      const float lse2 = total == 0 ? -INFINITY : top + __builtin_amdgcn_logf(total);
+      if (SHARED && !whole) sp.lse[part] = lse2;
+      else if (end.lse) end.lse[q_row[rt] * end.num_heads + head[rt]] = lse2 * kLn2;
+    }
+    __syncthreads();
+  }
+
+  if constexpr (!SHARED) break;
+  left -= to - from;
+  if (left <= 0) break;
+  // the next tile, of this request or of the next one that has any
+  from = 0;
+  if (++x.tile == tiles) {
+    tile0 += tiles;
+    do {
+      x = request_uniform(a, x.r + 1, cap);
+      extent<ROWS, BN>(a, x, group, &tiles, &steps);
+      tiles = uniform(tiles);
+      steps = uniform(steps);
+    } while (tiles == 0);
+  }
+  }
+  if (errs) raise(a.err, errs);
+}
+
+template <class E, int DP, int RT>
+void launch_attend(const AttendArgs& a, BlockDiv div, const Split& sp, hipStream_t stream) {
+  const int heads = a.cache.num_kv_heads;
+  if (sp.shares == 0) {
+    attend_fp4_kernel<E, DP, RT, false><<<dim3((unsigned)(sp.tiles * heads)), 256, 0, stream>>>(a, div, sp);
+    return;
+  }
+  const int64_t blocks = (int64_t)sp.tiles * heads;
+  const int64_t longest = a.batch.max_query_len < a.batch.num_tokens ? a.batch.max_query_len : a.batch.num_tokens;
+  const int64_t most = longest * (a.num_heads / heads) * a.cache.head_dim / 128;
+  int64_t several = 2048 / blocks;
+  several = several < most ? several : most;
+  several = several < 1 ? 1 : several < 16 ? several : 16;
+  attend_fp4_kernel<E, DP, RT, true><<<dim3((unsigned)(sp.shares * heads)), 256, 0, stream>>>(a, div, sp);
+  join_kernel<E, 16 * RT, 128><<<dim3((unsigned)blocks, (unsigned)several), 256, 0, stream>>>(a, sp);
+}
+
+template <class E, int RT>
+void launch_dims(const AttendArgs& a, BlockDiv div, const Split& sp, hipStream_t stream) {
+  if (a.cache.head_dim <= 64) launch_attend<E, 64, RT>(a, div, sp, stream);
+  else if (a.cache.head_dim <= 128) launch_attend<E, 128, RT>(a, div, sp, stream);
+  else launch_attend<E, 256, RT>(a, div, sp, stream);
+}
+
+template <class E>
+void launch_rows(const AttendArgs& a, BlockDiv div, const Split& sp, const Fp4Plan& p, hipStream_t stream) {
+  if (p.rows == 16) launch_dims<E, 1>(a, div, sp, stream);
+  else launch_dims<E, 2>(a, div, sp, stream);
+}
+
+}  // namespace
+
+hipError_t launch_attention_fp4(const AttendArgs& a, hipStream_t stream) {
+  const Fp4Plan p = plan_attention_fp4(a.cache, a.batch, a.num_heads);
+  Split sp = {fp4_shares_within(p, a.cache, a.workspace_bytes), p.tiles, nullptr, nullptr};
+  if (sp.shares > 0) {
+    sp.acc = (float*)a.workspace;  // first: rows of 16-byte vectors
+    sp.lse = sp.acc + (int64_t)(sp.shares + p.tiles) * a.cache.num_kv_heads * p.rows * a.cache.head_dim;
+  }
+  const BlockDiv div = block_div(a.cache.block_size);
+  if (a.cache.dtype == KVX_DTYPE_BF16) launch_rows<Bf16>(a, div, sp, p, stream);
+  else launch_rows<Fp16>(a, div, sp, p, stream);
+  return hipGetLastError();
+}
+
+int64_t attention_fp4_workspace(const kvx_paged_cache& c, const kvx_batch& b, int32_t num_heads) {
+  const Fp4Plan p = plan_attention_fp4(c, b, num_heads);
+  return p.shares > 0 ? (p.shares + (int64_t)p.tiles) * fp4_slot_bytes(p, c) : 0;
+}
+
+}  // namespace kvx

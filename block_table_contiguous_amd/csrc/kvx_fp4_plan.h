@@ -1,0 +1,51 @@
+// The launch shape of kvx_paged_attention_fp4, from the sizes of a call. Host code without any HIP call.
+#pragma once
+
+#include <stdint.h>
+
+#include "kvx_attention.h"
+
+namespace kvx {
+
+// A request's rows of one KV head are taken 16 or 32 at a time, by four wavefronts that take 32 slots each of every 128. Where the
+// tiles do not fill the GPU, or a batch's contexts are uneven, the batch's steps are shared out evenly (see Shares).
+constexpr int kFp4Fill = 768, kFp4MinSteps = 4;
+constexpr int64_t kFp4MaxWorkgroups = (1 << 24) - 1;  // of 256 threads: a launch has fewer than 2^32
+
+struct Fp4Plan {
+  int32_t rows, slots;  // of a tile and a step
+  int32_t tiles, shares;
+  int64_t busy;  // tiles that have rows, by the hints
+};
+inline Fp4Plan plan_attention_fp4(const kvx_paged_cache& c, const kvx_batch& b, int32_t num_heads) {
+  const int64_t group = num_heads / c.num_kv_heads;
+  const int64_t longest = b.max_query_len < b.num_tokens ? b.max_query_len : b.num_tokens;
+  Fp4Plan p;
+  p.rows = longest * group <= 16 ? 16 : 32;
+  p.slots = 128;
+  p.tiles = (int32_t)(b.num_tokens * group / p.rows + b.num_reqs);
+  int64_t busy = b.num_reqs * ((longest * group + p.rows - 1) / p.rows);
+  if (busy > p.tiles) busy = p.tiles;
+  if (busy < 1) busy = 1;
+  const int64_t context = b.max_context_len < 0x7fffffff ? b.max_context_len : 0x7fffffff;
+  const int fill = c.head_dim > 128 ? kFp4Fill / 3 : kFp4Fill;
+  int64_t shares = fill / c.num_kv_heads, most = busy * (context / p.slots) / kFp4MinSteps;
+  if (shares > most) shares = most;
+  p.busy = busy;
+  p.shares = busy * c.num_kv_heads < 4 * fill && shares > busy / 4 ? (int32_t)shares : 0;
+  return p;
+}
+
+// Bytes of a slot: a part of one tile of every KV head.
+inline int64_t fp4_slot_bytes(const Fp4Plan& p, const kvx_paged_cache& c) {
+  return (int64_t)c.num_kv_heads * p.rows * 4 * ((int64_t)c.head_dim + 1);
+}
+
+// The plan's shares in a workspace of so many bytes: fewer where it is too small for them, as long as they are more
+// workgroups than the tiles would be without sharing.
+inline int32_t fp4_shares_within(const Fp4Plan& p, const kvx_paged_cache& c, int64_t workspace_bytes) {
+  const int64_t fit = workspace_bytes / fp4_slot_bytes(p, c) - p.tiles;
+  return p.shares <= fit ? p.shares : fit > p.busy ? (int32_t)fit : 0;
+}
+
+}  // namespace kvx

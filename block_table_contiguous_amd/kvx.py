@@ -1,4 +1,5 @@
-"""Python binding of libkvx (include/kvx.h, include/kvx_attention.h): argument marshalling only.
+"""Python binding of libkvx (include/kvx.h, include/kvx_attention.h, include/kvx_fp4.h): argument
+marshalling only.
 
 Each kvx_* function here takes torch tensors, checks that they are device tensors of the
 right dtype and contiguity, and passes their data pointers, sizes and the current HIP stream
@@ -43,6 +44,7 @@ XFER_BYTES = 32  # sizeof(kvx_xfer)
 
 DTYPE_BF16, DTYPE_FP16 = 0, 1  # element types of the calls that compute (KVX_DTYPE_*)
 MAX_HEAD_DIM = 256
+FP4_GROUP = 32  # elements that share a scale in 4 bits (KVX_FP4_GROUP)
 MAX_AXES = 4
 
 _P = ctypes.c_void_p
@@ -60,6 +62,15 @@ class PagedCache(ctypes.Structure):
     tensor = None  # the tensor that it describes
 
 
+class Fp4Cache(ctypes.Structure):
+    """kvx_fp4_cache: paged blocks in 4 bits for the calls of kvx_fp4.h (see fp4_cache)."""
+
+    _fields_ = [("base", _P), ("num_blocks", _I64), ("block_stride_bytes", _I64), ("kv_stride_bytes", _I64),
+                ("head_stride_bytes", _I64), ("block_size", _I32), ("num_kv_heads", _I32), ("head_dim", _I32),
+                ("dtype", _I32)]
+    tensor = None  # the tensor that it describes
+
+
 class Batch(ctypes.Structure):
     """kvx_batch: the requests of one attention call."""
 
@@ -69,9 +80,9 @@ class Batch(ctypes.Structure):
 
 
 _F32 = ctypes.c_float
-_CACHE, _BATCH = ctypes.POINTER(PagedCache), ctypes.POINTER(Batch)
+_CACHE, _BATCH, _FP4 = ctypes.POINTER(PagedCache), ctypes.POINTER(Batch), ctypes.POINTER(Fp4Cache)
 
-# name -> (restype, argtypes); mirrors include/kvx.h and include/kvx_attention.h
+# name -> (restype, argtypes); mirrors include/kvx.h, include/kvx_attention.h and include/kvx_fp4.h
 SIGNATURES = {
     "kvx_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kvx_abi_version": (_I32, []),
@@ -102,6 +113,15 @@ SIGNATURES = {
     "kvx_evict_select": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _I32, _P, _I64, _I64, _I64, _P, _P, _P, _P]),
     "kvx_evict_compact": (ctypes.c_int, [_CACHE, _P, _I64, _I64, _P, _I64, _I64, _I32, _I32, _P, _I64, _P, _I64, _I64,
                                          _I64, _P, _I64, _I64, _I64, _P, _P]),
+    "kvx_fp4_plane_bytes": (_I64, [_I32, _I32]),
+    "kvx_rope_and_cache_fp4": (ctypes.c_int, [_FP4, _P, _I64, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _I32,
+                                              _P, _P, _I32, _I32, _P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P,
+                                              _P]),
+    "kvx_paged_attention_fp4": (ctypes.c_int, [_FP4, _BATCH, _P, _I64, _I64, _I32, _F32, _I32, _I64, _P, _I64, _I64, _P,
+                                               _P, _I64, _P, _P]),
+    "kvx_paged_attention_fp4_workspace": (_I64, [_FP4, _BATCH, _I32]),
+    "kvx_pack_fp4": (ctypes.c_int, [_CACHE, _P, _I32, _P, _P, _I64, _FP4, _P, _P]),
+    "kvx_unpack_fp4": (ctypes.c_int, [_FP4, _CACHE, _P, _I32, _P, _P, _I64, _P, _P]),
 }
 
 
@@ -864,3 +884,200 @@ def kvx_evict_compact(kv_cache, block_table, dst_block_table, keep, mass=None, m
     st = _F["kvx_evict_compact"](c, block_table.data_ptr(), *src, dst_block_table.data_ptr(), *dst, R, heads,
                                  keep.data_ptr(), budget, m_ptr, *m, mo_ptr, *mo, _ptr(err_flag), _stream(stream))
     _check("kvx_evict_compact", st)
+
+
+# ---------------------------------------------------------------------------------------
+# calls on a paged cache held in 4 bits (include/kvx_fp4.h)
+# ---------------------------------------------------------------------------------------
+
+_FP4_AXES = {"blocks_heads_kv": (0, 1, 2), "blocks_kv_heads": (0, 2, 1), "kv_blocks_heads": (1, 2, 0)}  # blocks, heads, K/V
+
+
+def fp4_plane_bytes(block_size: int, head_dim: int) -> int:
+    """Bytes of one head's K or V of a block in 4 bits: its rows' elements, then their scales."""
+    n = int(_F["kvx_fp4_plane_bytes"](int(block_size), int(head_dim)))
+    if n < 0:
+        raise ValueError(f"kvx: head_dim must be a multiple of {FP4_GROUP} up to {MAX_HEAD_DIM}, block_size at least 1")
+    return n
+
+
+def new_fp4_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int, device,
+                  layout: str = "blocks_heads_kv"):
+    """A zeroed 4-bit cache (or send buffer): uint8 in one of three layouts, [plane] as kvx_fp4.h
+    describes it:
+      blocks_heads_kv  [blocks][heads][K,V][plane]
+      blocks_kv_heads  [blocks][K,V][heads][plane]
+      kv_blocks_heads  [K,V][blocks][heads][plane]"""
+    import torch
+
+    if layout not in _FP4_AXES:
+        raise ValueError(f"unknown layout {layout}")
+    shape = [0, 0, 0, fp4_plane_bytes(block_size, head_dim)]
+    for axis, n in zip(_FP4_AXES[layout], (num_blocks, num_kv_heads, 2)):
+        shape[axis] = int(n)
+    return torch.zeros(shape, dtype=torch.uint8, device=device)
+
+
+def fp4_cache(kv_cache, head_dim: int, dtype, layout: str = "blocks_heads_kv") -> Fp4Cache:
+    """A 4-D uint8 tensor of new_fp4_cache's layouts (any strides whose planes are dense) as the
+    struct that the calls below take, for rows of head_dim elements and calls whose other rows are
+    of dtype. They make it from the tensor themselves; a caller that makes the same call many times
+    can make it once and pass it instead."""
+    import torch
+
+    shape, stride = kv_cache.shape, kv_cache.stride()
+    if layout not in _FP4_AXES:
+        raise ValueError(f"unknown layout {layout}")
+    b, h, w = _FP4_AXES[layout]
+    if kv_cache.dtype != torch.uint8 or len(shape) != 4 or shape[w] != 2:
+        raise ValueError("kvx: a 4-bit cache is a 4-D uint8 tensor of the given layout")
+    if stride[3] != 1:
+        raise ValueError("kvx: the planes of a 4-bit cache must be dense")
+    # a plane grows by more than its padding with every token, so its size says how many there are
+    tokens = shape[3] * FP4_GROUP // (17 * head_dim) if head_dim > 0 else 0
+    if tokens < 1 or fp4_plane_bytes(tokens, head_dim) != shape[3]:
+        raise ValueError("kvx: the last dimension of a 4-bit cache must be fp4_plane_bytes(block_size, head_dim)")
+    # the stride of a dimension with one entry is never used and may be anything
+    c = Fp4Cache(kv_cache.data_ptr(), shape[b], stride[b] if shape[b] > 1 else 0, stride[w],
+                 stride[h] if shape[h] > 1 else 0, tokens, shape[h], head_dim, _dtype_code(dtype, "dtype"))
+    c.tensor = kv_cache  # kept alive, and looked at for its device
+    return c
+
+
+def _fp4(kv_cache, rows, layout) -> Fp4Cache:
+    """kv_cache for a call whose rows are [tokens][heads][head_dim] like `rows`."""
+    if type(kv_cache) is Fp4Cache:
+        return kv_cache
+    if rows.dim() != 3:
+        raise ValueError("kvx: rows must be [num_tokens][heads][head_dim]")
+    return fp4_cache(kv_cache, rows.shape[2], rows.dtype, layout)
+
+
+def kvx_rope_and_cache_fp4(query, key, value, positions, inv_freq, pair_axis: Sequence[int], slot_mapping, kv_cache,
+                           query_out, key_out=None, value_out=None, layout: str = "blocks_heads_kv",
+                           interleaved: bool = False, err_flag=None, stream=None):
+    """kvx_rope_and_cache into a 4-bit cache (a tensor of new_fp4_cache's layouts, or fp4_cache of
+    it). key_out and value_out ([num_tokens][num_kv_heads][head_dim], both or neither) get what the
+    cache then holds of each token; they must not overlap key and value."""
+    import torch
+
+    c = _fp4(kv_cache, key, layout)
+    _want(slot_mapping, torch.int64, "slot_mapping")
+    _want(positions, torch.int64, "positions")
+    _want(inv_freq, torch.float32, "inv_freq")
+    T = slot_mapping.numel()
+    axes = positions.shape
+    if len(axes) != 2 or axes[1] != T:
+        raise ValueError("kvx: positions must be [num_axes][num_tokens]")
+    pairs = len(pair_axis)
+    if inv_freq.numel() != pairs:
+        raise ValueError("kvx: pair_axis and inv_freq need one entry a pair")
+    if (query is None) != (query_out is None):
+        raise ValueError("kvx: query and query_out go together")
+    if (key_out is None) != (value_out is None):
+        raise ValueError("kvx: key_out and value_out go together")
+    ks = _rows(key, T, c.num_kv_heads, c, "key")
+    vs = _rows(value, T, c.num_kv_heads, c, "value")
+    heads, qs, os_, q_ptr, o_ptr = 0, (0, 0), (0, 0), None, None
+    if query is not None:
+        qs = _rows(query, T, None, c, "query")
+        heads = query.shape[1]
+        os_ = _rows(query_out, T, heads, c, "query_out")
+        q_ptr, o_ptr = query.data_ptr(), query_out.data_ptr()
+    kos, vos, ko_ptr, vo_ptr = (0, 0), (0, 0), None, None
+    if key_out is not None:
+        kos = _rows(key_out, T, c.num_kv_heads, c, "key_out")
+        vos = _rows(value_out, T, c.num_kv_heads, c, "value_out")
+        ko_ptr, vo_ptr = key_out.data_ptr(), value_out.data_ptr()
+    _on_current_device((query, key, value, positions, inv_freq, slot_mapping, c.tensor, query_out, key_out, value_out,
+                        err_flag))
+    axis_of = array("i", pair_axis if pairs else (0,))
+    st = _F["kvx_rope_and_cache_fp4"](
+        c, q_ptr, *qs, heads, key.data_ptr(), *ks, value.data_ptr(), *vs, T, positions.data_ptr(), axes[0],
+        axis_of.buffer_info()[0], inv_freq.data_ptr(), 2 * pairs, bool(interleaved), slot_mapping.data_ptr(),
+        o_ptr, *os_, ko_ptr, *kos, vo_ptr, *vos, _ptr(err_flag), _stream(stream))
+    _check("kvx_rope_and_cache_fp4", st)
+
+
+def attention_workspace_fp4_bytes(query, kv_cache, num_reqs: int, max_query_len: int, max_context_len: int,
+                                  layout: str = "blocks_heads_kv") -> int:
+    """Bytes of workspace with which kvx_paged_attention_fp4 splits such a batch as far as pays."""
+    c = _fp4(kv_cache, query, layout)
+    b = Batch(None, None, None, 0, 0, query.shape[0], int(max_query_len), int(max_context_len), int(num_reqs))
+    n = _F["kvx_paged_attention_fp4_workspace"](c, b, query.shape[1])
+    if n < 0:
+        raise ValueError("kvx: kvx_paged_attention_fp4 does not take a batch of these sizes")
+    return int(n)
+
+
+def new_attention_workspace_fp4(query, kv_cache, num_reqs: int, max_query_len: int, max_context_len: int,
+                                layout: str = "blocks_heads_kv"):
+    """A workspace of attention_workspace_fp4_bytes (one per concurrent stream or captured graph)."""
+    import torch
+
+    n = attention_workspace_fp4_bytes(query, kv_cache, num_reqs, max_query_len, max_context_len, layout)
+    return torch.empty(n, dtype=torch.uint8, device=query.device)
+
+
+def kvx_paged_attention_fp4(query, kv_cache, block_table, q_offsets, context_lens, out, lse=None,
+                            scale: Optional[float] = None, causal: bool = True, window: int = 0,
+                            max_query_len: Optional[int] = None, max_context_len: Optional[int] = None,
+                            workspace=None, layout: str = "blocks_heads_kv", err_flag=None, stream=None):
+    """kvx_paged_attention over a 4-bit cache (a tensor of new_fp4_cache's layouts, or fp4_cache of
+    it), with a workspace of new_attention_workspace_fp4."""
+    c = _fp4(kv_cache, query, layout)
+    b, heads, qs = _batch(query, c, block_table, q_offsets, context_lens, max_query_len, max_context_len)
+    os_ = _rows(out, b.num_tokens, heads, c, "out")
+    if lse is not None:
+        _want_lse(lse, b.num_tokens, heads)
+    nbytes = 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("kvx: workspace must be contiguous")
+        nbytes = workspace.numel() * workspace.element_size()
+    _on_current_device((query, c.tensor, block_table, q_offsets, context_lens, out, lse, workspace, err_flag))
+    st = _F["kvx_paged_attention_fp4"](
+        c, b, query.data_ptr(), *qs, heads, c.head_dim ** -0.5 if scale is None else float(scale), bool(causal),
+        int(window), out.data_ptr(), *os_, _ptr(lse), _ptr(workspace), nbytes, _ptr(err_flag), _stream(stream))
+    _check("kvx_paged_attention_fp4", st)
+
+
+def _transfer_fp4(layer_bases, kv_cache, xfers, xfer_count, total_blocks: int, buffer, layout, buffer_layout,
+                  err_flag):
+    """(cache, buffer) structs of a transfer between 16-bit layers like kv_cache and 4-bit blocks."""
+    import torch
+
+    c = _cache(kv_cache, layout)
+    f = buffer if type(buffer) is Fp4Cache else fp4_cache(
+        buffer, c.head_dim, torch.bfloat16 if c.dtype == DTYPE_BF16 else torch.float16, buffer_layout)
+    _want(layer_bases, torch.int64, "layer_bases")
+    _want_runs(xfers, xfer_count, total_blocks)
+    if (f.block_size, f.num_kv_heads, f.head_dim, f.dtype) != (c.block_size, c.num_kv_heads, c.head_dim, c.dtype):
+        raise ValueError("kvx: the caches and the 4-bit blocks must have the same sizes")
+    if f.num_blocks < layer_bases.numel() * int(total_blocks):
+        raise ValueError("kvx: the 4-bit blocks are fewer than num_layers * total_blocks")
+    _on_current_device((layer_bases, xfers, xfer_count, c.tensor, f.tensor, err_flag))
+    return c, f
+
+
+def kvx_pack_fp4(layer_bases, kv_cache, xfers, xfer_count, total_blocks: int, send_buf, layout: str = "blocks_tokens_kv",
+                 buffer_layout: str = "blocks_heads_kv", err_flag=None, stream=None):
+    """Quantise the listed blocks of every layer into send_buf, num_layers * total_blocks 4-bit
+    blocks (new_fp4_cache, or fp4_cache of it), layer by layer. kv_cache is one of the layers' 5-D
+    tensors (or paged_cache of it): all have its sizes and strides."""
+    c, f = _transfer_fp4(layer_bases, kv_cache, xfers, xfer_count, total_blocks, send_buf, layout,
+                         buffer_layout, err_flag)
+    st = _F["kvx_pack_fp4"](c, _ptr(layer_bases), layer_bases.numel(), _ptr(xfers), _ptr(xfer_count), int(total_blocks), f,
+                            _ptr(err_flag), _stream(stream))
+    _check("kvx_pack_fp4", st)
+
+
+def kvx_unpack_fp4(send_buf, layer_bases, kv_cache, xfers, xfer_count, total_blocks: int,
+                   layout: str = "blocks_tokens_kv", buffer_layout: str = "blocks_heads_kv", err_flag=None, stream=None):
+    """Write the 4-bit blocks of send_buf, as kvx_pack_fp4 leaves them, into the listed blocks of
+    every layer's 16-bit cache; kv_cache as there."""
+    c, f = _transfer_fp4(layer_bases, kv_cache, xfers, xfer_count, total_blocks, send_buf, layout,
+                         buffer_layout, err_flag)
+    st = _F["kvx_unpack_fp4"](f, c, _ptr(layer_bases), layer_bases.numel(), _ptr(xfers), _ptr(xfer_count),
+                              int(total_blocks), _ptr(err_flag), _stream(stream))
+    _check("kvx_unpack_fp4", st)
