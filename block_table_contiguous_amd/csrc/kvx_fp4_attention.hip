@@ -434,34 +434,449 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(Atte
   if (errs) raise(a.err, errs);
 }
 
-template <class E, int DP, int RT>
-void launch_attend(const AttendArgs& a, BlockDiv div, const Split& sp, hipStream_t stream) {
+// In the 32x32x16 products lane l holds column (or row) l % 32 and, with hf = l / 32, elements 8 hf to 8 hf + 7 of the summed
+// dimension; result register i of lane l is row 8 (i / 4) + 4 hf + i % 4, column l % 32.
+__device__ __forceinline__ f32x16 product(Bf16, u32x4 a, u32x4 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(Bf16::V8, a), __builtin_bit_cast(Bf16::V8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 product(Fp16, u32x4 a, u32x4 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(Fp16::V8, a), __builtin_bit_cast(Fp16::V8, b), c, 0, 0, 0);
+}
+
+// Many rows: 128 of them a workgroup, 32 a wavefront, and 64 slots a step, which the four wavefronts widen to 16 bits on their
+// way to LDS, 16 slots each. Scores transposed as above, with the 32x32x16 products.
+//   BY_BLOCK: 16 slots always lie in one block, whose address is formed once a wavefront, in scalar registers.
+//   SHARED: the grid's workgroups take equal shares of the whole batch's steps (see Shares).
+template <class E, int DP, bool BY_BLOCK, bool SHARED>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_rows_kernel(AttendArgs args, BlockDiv div, Split sp) {
+  const AttendArgs a = argument<AttendArgs>();
+  constexpr int ROWS = 128, BN = 64, KW = 16, KT = 2, KSTEPS = DP / 16, DT = DP / 32;
+  constexpr int KS = DP > 128 ? 2 : 1;                   // groups of K, and of V, that a lane stages
+  constexpr int KROW = DP * 2 + 16, VROW = DP * 2 + 64;  // bytes of a row in LDS
+  __shared__ __align__(16) char smem[BN * (KROW + VROW) + BN];
+  char* const sk = smem;
+  char* const sv = smem + BN * KROW;
+  uint8_t* const flags = (uint8_t*)(smem + BN * (KROW + VROW));
+
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform((int32_t)(tid >> 6));
+  const int n = lane & 31, hf = lane >> 5;
+  const int group = a.num_heads / a.cache.num_kv_heads, dim = a.cache.head_dim, groups = dim / kGroup;
+  const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size;
+  int g = blockIdx.x % a.cache.num_kv_heads, index = blockIdx.x / a.cache.num_kv_heads;
+  if constexpr (SHARED) {  // shares that follow one another to one XCD: workgroup i runs on XCD i % 8
+    const int xcd = blockIdx.x % 8, per = gridDim.x / 8, more = gridDim.x % 8;
+    const int at = xcd * per + (xcd < more ? xcd : more) + blockIdx.x / 8;
+    g = at / sp.shares;
+    index = at - g * sp.shares;
+  }
+  if (blockIdx.x == 0) check_batch(a, cap, tid, 256);
+
+  // lane 16 q + s stages group q (and q + 4) of slot s of its wavefront's 16
+  const int slot = lane & 15, quarter = lane >> 4;
+  char* const sk_put = sk + (w * KW + slot) * KROW + quarter * 64;
+  char* const sv_put = sv + (w * KW + slot) * VROW + quarter * 64;
+  const char* const sk_get = sk + n * KROW + hf * 16;
+  const char* const sv_get = sv + (4 * hf + ((lane & 15) >> 2)) * VROW + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+
+  Rows x;
+  Shares all;
+  int32_t tiles = 0, steps = 1, from = 0, to = 1;  // steps [from, to) of tile x.tile
+  uint32_t tile0 = 0;
+  int64_t left = 1;
+  if constexpr (SHARED) {
+    const Requests q = locate<ROWS, BN>(a, group, cap, lane, sp.shares, &all, [&](const Shares& s, const Requests& q) {
+      const int64_t begin = share_begin(s, index);
+      return index < s.count && q.step0 <= begin && begin < q.step0 + (int64_t)q.tiles * q.steps;
+    });
+    if (q.steps == 0) return;
+    const int64_t begin = share_begin(all, index);
+    left = share_begin(all, index + 1) - begin;
+    tile0 = q.tile0;
+    tiles = q.tiles;
+    steps = q.steps;
+    x = q.x;
+    x.tile = (int32_t)quotient(begin - q.step0, steps);
+    from = (int32_t)(begin - q.step0 - (int64_t)x.tile * steps);
+  } else {
+    // The longest tiles first; every other round of 256 workgroups (one a CU) the other way round, so that a CU's second
+    // tile makes up for its first.
+    const int per = 256 / a.cache.num_kv_heads > 0 ? 256 / a.cache.num_kv_heads : 1, round = index / per;
+    const int back = (round + 1) * per < sp.tiles ? (round + 1) * per : sp.tiles;
+    x = find_rows<ROWS>(a, sp.tiles - 1 - (round & 1 ? back - 1 - (index - round * per) : index), group, cap, lane);
+    if (x.tile < 0 || (int64_t)x.tile * ROWS >= (int64_t)x.tokens * group) return;
+  }
+  int errs = 0;
+  bool bad_blocks = false;
+  for (;;) {
+  const AttendArgs a = argument<AttendArgs>();
+  if constexpr (SHARED) {
+    if (tile0 + x.tile >= (uint32_t)sp.tiles) break;  // offsets that are not a CSR: the workspace has no slots for more
+    to = from + left < steps ? (int)(from + left) : steps;
+  }
+  const int row0 = x.tile * ROWS, rows = x.tokens * group;
+
+  // this lane's row, what it sees, and what any row of the workgroup sees
+  const int row = row0 + w * 32 + n;
+  const bool used = row < rows;
+  const int token = used ? row / group : 0, head = g * group + (used ? row - token * group : 0);
+  const int64_t q_row = x.q0 + token;
+  int2 see = sees(a, x, token);
+  if (!used) see = {0, 0};
+  const int last_row = row0 + ROWS < rows ? row0 + ROWS - 1 : rows - 1;
+  const int2 first = sees_uniform(a, x, row0 / group), last = sees_uniform(a, x, last_row / group);
+  const int kend = last.y;
+  const int t_first = first.x / BN, t_all = (kend + BN - 1) / BN - t_first;
+  int tb = t_first, te = t_first + (t_all > 0 ? t_all : 0);
+  if constexpr (SHARED) {
+    if (t_all == steps) {
+      tb = t_first + from;
+      te = t_first + to;
+    } else {  // a tile whose rows see less than all of the request's: its steps in proportion
+      const int64_t mine = te - tb;
+      te = tb + (int)quotient(mine * to, steps);
+      tb = tb + (int)quotient(mine * from, steps);
+    }
+  }
+  tb = uniform(tb);
+  te = uniform(te);
+
+  // q: lane n's row, eight elements a step
+  u32x4 q[KSTEPS];
+  {
+    const char* p = a.query.base + q_row * a.query.token_stride + head * a.query.head_stride;
+#pragma unroll
+    for (int s = 0; s < KSTEPS; ++s) {
+      q[s] = u32x4{0, 0, 0, 0};
+      if (used && 2 * s + hf < dim / 8) q[s] = gload<u32x4>(p + (2 * s + hf) * 16);
+    }
+  }
+
+  const char* const base = (const char*)a.cache.base + g * a.cache.head_stride_bytes;
+  const int64_t scales = (int64_t)a.cache.block_size * (dim / 2);
+  const int32_t* const table = a.batch.block_table + x.r * a.batch.bt_row_stride;
+  const int cols = (int)a.batch.max_blocks_per_req;
+
+  f32x16 acc[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) acc[d] = f32x16{};
+  float m = -INFINITY, l = 0;
+  const float c1 = a.scale * kLog2e;
+
+  auto load_id = [&](int t) -> int32_t {
+    const int b = block_of(div, t * BN + w * KW + (BY_BLOCK ? 0 : slot));
+    return gload<int32_t>(table + (b < cols ? b : cols - 1));
+  };
+  u32x4 rk[KS], rv[KS];
+  uint32_t ks[KS], vs[KS];
+  uint32_t ok_mask = 0;
+  auto fetch = [&](int t, int32_t id) {
+    // a slot that is not there is read from the cache's first rows; its scale of V becomes 0, and its weight is
+    const int j = t * BN + w * KW + (BY_BLOCK ? 0 : slot);
+    const char *e, *s;
+    if constexpr (BY_BLOCK) {
+      const int32_t block = uniform(id);
+      int there = kend - j < 16 ? kend - j : 16;
+      if (there < 0) there = 0;
+      ok_mask = 0;
+      const char* k = base;
+      int o = 0;
+      if ((uint32_t)block < (uint64_t)a.cache.num_blocks) {
+        k += block * a.cache.block_stride_bytes;
+        o = j - block_of(div, j) * div.size;
+        ok_mask = (1u << there) - 1;
+      } else if (there > 0) {
+        bad_blocks = true;
+      }
+      e = k + (int64_t)o * (dim / 2) + slot * (dim / 2);
+      s = k + scales + (int64_t)o * groups + slot * groups;
+    } else {
+      const bool in = j < kend, ok = in && (uint32_t)id < (uint64_t)a.cache.num_blocks;
+      if (in && !ok) errs |= KVX_DEVERR_BLOCK_RANGE;
+      ok_mask = (uint32_t)(__ballot(ok) & 0xffff);
+      const int64_t o = ok ? j - block_of(div, j) * div.size : 0;
+      const char* k = base + (ok ? id * a.cache.block_stride_bytes : 0);
+      e = k + o * (dim / 2);
+      s = k + scales + o * groups;
+    }
+#pragma unroll
+    for (int c = 0; c < KS; ++c) {
+      const int at = c * 4 + quarter;
+      rk[c] = rv[c] = u32x4{0, 0, 0, 0};
+      ks[c] = vs[c] = 0;
+      if (at < groups) {
+        rk[c] = gload<u32x4>(e + at * 16);
+        ks[c] = gload<uint8_t>(s + at);
+        rv[c] = gload<u32x4>(e + at * 16 + a.cache.kv_stride_bytes);
+        vs[c] = gload<uint8_t>(s + at + a.cache.kv_stride_bytes);
+      }
+    }
+  };
+
+  int32_t id = 0;
+  if (tb < te) {
+    fetch(tb, load_id(tb));
+    id = load_id(tb + 1);
+  }
+  // q is here before the loop: a wait for it inside would be one for the loads in flight as well
+#pragma unroll
+  for (int st = 0; st < KSTEPS; ++st) asm volatile("" : "+v"(q[st]));
+  for (int t = tb; t < te; ++t) {
+    const int k0 = t * BN;
+    // every row sees every slot of an inner tile
+    const bool inner = k0 >= last.x && k0 + BN <= first.y;
+    if (lane < KW) flags[w * KW + lane] = (ok_mask >> lane) & 1;
+    if (ok_mask != 0xffff) {
+#pragma unroll
+      for (int c = 0; c < KS; ++c)
+        if (!(ok_mask >> here(slot) & 1)) ks[c] = vs[c] = 0;
+    }
+    if (!inner) {
+      // A weight of zero times a NaN or infinity is NaN: slots of V that may read back as one are left out of the products and
+      // added below for the rows that see them.
+      uint64_t bad = 0;
+#pragma unroll
+      for (int c = 0; c < KS; ++c) bad |= __ballot(vs[c] > kFiniteScales<E>);
+      bad |= bad >> 32;
+      bad |= bad >> 16;
+      if ((bad >> here(slot)) & 1) {
+#pragma unroll
+        for (int c = 0; c < KS; ++c) vs[c] = 0, rv[c] = u32x4{0, 0, 0, 0};
+        if (quarter == 0) flags[w * KW + slot] = 3;
+      }
+    }
+    if (DP >= 128 || quarter * 32 < DP) {
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        const float k_scale = scale_of(ks[c]), v_scale = scale_of(vs[c]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          *(u32x4*)(sk_put + c * 256 + k * 16) = decode<E>(rk[c][k], k_scale);
+          *(u32x4*)(sv_put + c * 256 + k * 16) = decode<E>(rv[c][k], v_scale);
+        }
+      }
+    }
+    lds_barrier();
+    if (t + 1 < te) {
+      fetch(t + 1, id);
+      id = load_id(t + 2);
+    }
+
+    const uint8_t flag = flags[lane];
+    // one bit a slot
+    const uint64_t there = __ballot(flag & 1), skipped = __ballot(flag & 2);
+    // The wavefront that has begun on a tile goes first until it is done: the SIMD's other one does its own part better
+    // while these products run.
+    __builtin_amdgcn_s_setprio(1);
+    f32x16 s[KT];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) s[kt] = f32x16{};
+#pragma unroll
+    for (int st = 0; st < KSTEPS; ++st)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)  // no product waits for the one before it
+        s[kt] = product(E(), *(const u32x4*)(sk_get + kt * 32 * KROW + st * 32), q[st], s[kt]);
+    // K is read eight pieces ahead of the products: read as they are needed, each would wait for LDS
+    if constexpr (KT * KSTEPS > 8) {
+      __builtin_amdgcn_sched_group_barrier(kDsRead, 8, 0);
+#pragma unroll
+      for (int i = 0; i < KT * KSTEPS - 8; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(kMfma, 8, 0);
+    }
+    if (!inner || ~there) {
+      const int at = here(k0 + 4 * hf), lo = see.x - at, hi = see.y - at;
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        const uint32_t mine = (uint32_t)(there >> (kt * 32)) >> here(4 * hf);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int o = 8 * (i / 4) + i % 4;
+          if (kt * 32 + o < lo || kt * 32 + o >= hi || !(mine & (1u << o))) s[kt][i] = -INFINITY;
+        }
+      }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kt][i]);
+    top = fmaxf(top, other_half(top)) * c1;
+    // the reference moves only when the maximum leaves its range: the sums keep their 32 bits
+    if (__any(top > m + (kLift<E> + kLag<E>))) {
+      const float held = m, now = here(top);
+      const float to = now - held > kLift<E> + kLag<E> ? (is_far(now) ? now : now - kLift<E>) : held;
+      const float shrink = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(held - to);
+      m = to;
+      l *= shrink;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[d][i] *= shrink;
+    }
+    if (__any(is_far(m))) {
+      // the scores become what they stand above the reference, rounded before it is taken from them, as the maximum was
+      const float from = m == -INFINITY ? 0.0f : m, factor = here(c1), back = 1.0f / factor;
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float up = rounded_difference(rounded_product(s[kt][i], factor), from);
+          if (is_far(from)) s[kt][i] = up * back;
+        }
+    }
+    const float ref = m == -INFINITY || is_far(m) ? 0.0f : m;
+    // Weights and products by 16 slots: V is read one group ahead, and the weights of a group are formed in the shadow of
+    // the products of the one before.
+#pragma unroll
+    for (int gr = 0; gr < 2 * KT; ++gr) {
+      f32x8 pv;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = 8 * (gr % 2) + i;
+        pv[i] = s[gr / 2][at] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[gr / 2][at], c1, -ref));
+        l += pv[i];
+      }
+      // one rounding of each weight to the element type, which the matrix unit takes
+      const u32x4 p = narrow<E>(pv);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const char* at = sv_get + 16 * gr * VROW + d * 64;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KVX_LDS s16x4*)at);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KVX_LDS s16x4*)(at + 8 * VROW));
+        const s16x8 va = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        acc[d] = product(E(), __builtin_bit_cast(u32x4, va), p, acc[d]);
+      }
+    }
+    __builtin_amdgcn_sched_group_barrier(kDsRead, 2 * DT, 1);
+    __builtin_amdgcn_sched_group_barrier(kVector, 28, 1);
+#pragma unroll
+    for (int gr = 0; gr < 2 * KT; ++gr) {
+      if (gr + 1 < 2 * KT) __builtin_amdgcn_sched_group_barrier(kDsRead, 2 * DT, 1);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 1);
+        if (gr + 1 < 2 * KT) __builtin_amdgcn_sched_group_barrier(kVector, 28 / DT, 1);
+      }
+    }
+    __builtin_amdgcn_s_setprio(0);
+    if (skipped) {
+      for (uint64_t todo = skipped; todo; todo &= todo - 1) {
+        const int o = __builtin_ctzll(todo), j = k0 + o;
+        float pj = 0;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (kt * 32 + 8 * (i / 4) + i % 4 == o - here(4 * hf)) pj = s[kt][i];
+        pj += other_half(pj);
+        if (j < see.x || j >= see.y) continue;
+        const int b = block_of(div, j), in = j - b * div.size;
+        const char* plane = base + table[b] * a.cache.block_stride_bytes + a.cache.kv_stride_bytes;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          if (d >= groups) break;
+          const float scale = scale_of(gload<uint8_t>(plane + scales + (int64_t)in * groups + d));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x4 v = decode4<E>(gload<uint16_t>(plane + (int64_t)in * (dim / 2) + d * 16 + i * 4 + hf * 2), scale);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[d][4 * i + e] += pj * v[e];
+          }
+          __builtin_amdgcn_sched_barrier(0);  // a few at a time: this branch must not set the registers of the loop
+        }
+      }
+    }
+    lds_barrier();
+  }
+  l += other_half(l);
+
+  const AttendArgs end = argument<AttendArgs>();
+  const bool whole = !SHARED || (from == 0 && to == steps);
+  const float inv = l == 0 ? 0.0f : 1.0f / l;
+  // where a part's row goes: share index of tile tile0 + x.tile
+  const int64_t part = ((int64_t)(index + (int32_t)(tile0 + x.tile)) * end.cache.num_kv_heads + g) * ROWS + (row - row0);
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = d * 32 + 8 * i + 4 * hf;
+      if (!used || e >= end.cache.head_dim) continue;
+      f32x4 v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = l == 0 ? 0.0f : acc[d][4 * i + k] * inv;
+      if (SHARED && !whole) {
+        gstore(sp.acc + part * end.cache.head_dim + e, v);
+      } else {
+        gstore((char*)end.out.base + q_row * end.out.token_stride + head * end.out.head_stride + e * 2,
+               __builtin_convertvector(v, typename E::V4));
+      }
+    }
+  if (used && hf == 0) {
+    const float lse2 = l == 0 ? -INFINITY : m + __builtin_amdgcn_logf(l);
+    if (SHARED && !whole) sp.lse[part] = lse2;
+    else if (end.lse) end.lse[q_row * end.num_heads + head] = lse2 * kLn2;
+  }
+
+  if constexpr (!SHARED) break;
+  left -= to - from;
+  if (left <= 0) break;
+  // the next tile, of this request or of the next one that has any
+  from = 0;
+  if (++x.tile == tiles) {
+    tile0 += tiles;
+    do {
+      x = request_uniform(a, x.r + 1, cap);
+      extent<ROWS, BN>(a, x, group, &tiles, &steps);
+      tiles = uniform(tiles);
+      steps = uniform(steps);
+    } while (tiles == 0);
+  }
+  }
+  if (bad_blocks) errs |= KVX_DEVERR_BLOCK_RANGE;
+  if (errs) raise(a.err, errs);
+}
+
+template <class E, int DP>
+void launch_attend(const AttendArgs& a, BlockDiv div, const Split& sp, int rows, hipStream_t stream) {
   const int heads = a.cache.num_kv_heads;
+  const bool by_block = a.cache.block_size % 16 == 0;
   if (sp.shares == 0) {
-    attend_fp4_kernel<E, DP, RT, false><<<dim3((unsigned)(sp.tiles * heads)), 256, 0, stream>>>(a, div, sp);
+    const dim3 grid((unsigned)(sp.tiles * heads));
+    if (rows == 16) attend_fp4_kernel<E, DP, 1, false><<<grid, 256, 0, stream>>>(a, div, sp);
+    else if (rows == 32) attend_fp4_kernel<E, DP, 2, false><<<grid, 256, 0, stream>>>(a, div, sp);
+    else if (by_block) attend_fp4_rows_kernel<E, DP, true, false><<<grid, 256, 0, stream>>>(a, div, sp);
+    else attend_fp4_rows_kernel<E, DP, false, false><<<grid, 256, 0, stream>>>(a, div, sp);
     return;
   }
+  const dim3 grid((unsigned)(sp.shares * heads));
+  // a tile's rows are joined by one workgroup, or by several while that is up to 2048 in all and they have 32 threads' work each
   const int64_t blocks = (int64_t)sp.tiles * heads;
   const int64_t longest = a.batch.max_query_len < a.batch.num_tokens ? a.batch.max_query_len : a.batch.num_tokens;
   const int64_t most = longest * (a.num_heads / heads) * a.cache.head_dim / 128;
   int64_t several = 2048 / blocks;
   several = several < most ? several : most;
   several = several < 1 ? 1 : several < 16 ? several : 16;
-  attend_fp4_kernel<E, DP, RT, true><<<dim3((unsigned)(sp.shares * heads)), 256, 0, stream>>>(a, div, sp);
-  join_kernel<E, 16 * RT, 128><<<dim3((unsigned)blocks, (unsigned)several), 256, 0, stream>>>(a, sp);
-}
-
-template <class E, int RT>
-void launch_dims(const AttendArgs& a, BlockDiv div, const Split& sp, hipStream_t stream) {
-  if (a.cache.head_dim <= 64) launch_attend<E, 64, RT>(a, div, sp, stream);
-  else if (a.cache.head_dim <= 128) launch_attend<E, 128, RT>(a, div, sp, stream);
-  else launch_attend<E, 256, RT>(a, div, sp, stream);
+  const dim3 join((unsigned)blocks, (unsigned)several);
+  if (rows == 16) {
+    attend_fp4_kernel<E, DP, 1, true><<<grid, 256, 0, stream>>>(a, div, sp);
+    join_kernel<E, 16, 128><<<join, 256, 0, stream>>>(a, sp);
+  } else if (rows == 32) {
+    attend_fp4_kernel<E, DP, 2, true><<<grid, 256, 0, stream>>>(a, div, sp);
+    join_kernel<E, 32, 128><<<join, 256, 0, stream>>>(a, sp);
+  } else {
+    if (by_block) attend_fp4_rows_kernel<E, DP, true, true><<<grid, 256, 0, stream>>>(a, div, sp);
+    else attend_fp4_rows_kernel<E, DP, false, true><<<grid, 256, 0, stream>>>(a, div, sp);
+    join_kernel<E, 128, 64><<<join, 256, 0, stream>>>(a, sp);
+  }
 }
 
 template <class E>
-void launch_rows(const AttendArgs& a, BlockDiv div, const Split& sp, const Fp4Plan& p, hipStream_t stream) {
-  if (p.rows == 16) launch_dims<E, 1>(a, div, sp, stream);
-  else launch_dims<E, 2>(a, div, sp, stream);
+void launch_dims(const AttendArgs& a, BlockDiv div, const Split& sp, int rows, hipStream_t stream) {
+  if (a.cache.head_dim <= 64) launch_attend<E, 64>(a, div, sp, rows, stream);
+  else if (a.cache.head_dim <= 128) launch_attend<E, 128>(a, div, sp, rows, stream);
+  else launch_attend<E, 256>(a, div, sp, rows, stream);
 }
 
 }  // namespace
@@ -474,8 +889,8 @@ hipError_t launch_attention_fp4(const AttendArgs& a, hipStream_t stream) {
     sp.lse = sp.acc + (int64_t)(sp.shares + p.tiles) * a.cache.num_kv_heads * p.rows * a.cache.head_dim;
   }
   const BlockDiv div = block_div(a.cache.block_size);
-  if (a.cache.dtype == KVX_DTYPE_BF16) launch_rows<Bf16>(a, div, sp, p, stream);
-  else launch_rows<Fp16>(a, div, sp, p, stream);
+  if (a.cache.dtype == KVX_DTYPE_BF16) launch_dims<Bf16>(a, div, sp, p.rows, stream);
+  else launch_dims<Fp16>(a, div, sp, p.rows, stream);
   return hipGetLastError();
 }
 

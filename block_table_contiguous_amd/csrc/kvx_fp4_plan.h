@@ -7,9 +7,10 @@
 
 namespace kvx {
 
-// A request's rows of one KV head are taken 16 or 32 at a time, by four wavefronts that take 32 slots each of every 128. Where the
-// tiles do not fill the GPU, or a batch's contexts are uneven, the batch's steps are shared out evenly (see Shares).
-constexpr int kFp4Fill = 768, kFp4MinSteps = 4;
+// A request's rows of one KV head are taken 16 or 32 at a time, by four wavefronts that take 32 slots each of every 128, or, where there
+// are more, 128 at a time, 64 slots a step. Where the tiles do not fill the GPU, or a decode batch's contexts are uneven, the
+// batch's steps are shared out evenly (see Shares) to as many workgroups as the GPU holds, of kFp4MinSteps steps at least.
+constexpr int kFp4FillFew = 768, kFp4Fill = 512, kFp4MinSteps = 4;
 constexpr int64_t kFp4MaxWorkgroups = (1 << 24) - 1;  // of 256 threads: a launch has fewer than 2^32
 
 struct Fp4Plan {
@@ -21,18 +22,22 @@ inline Fp4Plan plan_attention_fp4(const kvx_paged_cache& c, const kvx_batch& b, 
   const int64_t group = num_heads / c.num_kv_heads;
   const int64_t longest = b.max_query_len < b.num_tokens ? b.max_query_len : b.num_tokens;
   Fp4Plan p;
-  p.rows = longest * group <= 16 ? 16 : 32;
-  p.slots = 128;
+  p.rows = longest * group <= 16 ? 16 : longest * group <= 32 ? 32 : 128;
+  // tiles of few rows also have to be few enough for a launch, as those of requests that keep to the hint are
+  if ((b.num_tokens * group / p.rows + b.num_reqs) * c.num_kv_heads > kFp4MaxWorkgroups) p.rows = 128;
+  const bool few = p.rows < 128;
+  p.slots = few ? 128 : 64;
   p.tiles = (int32_t)(b.num_tokens * group / p.rows + b.num_reqs);
   int64_t busy = b.num_reqs * ((longest * group + p.rows - 1) / p.rows);
   if (busy > p.tiles) busy = p.tiles;
   if (busy < 1) busy = 1;
   const int64_t context = b.max_context_len < 0x7fffffff ? b.max_context_len : 0x7fffffff;
-  const int fill = c.head_dim > 128 ? kFp4Fill / 3 : kFp4Fill;
+  const int all = few ? kFp4FillFew : kFp4Fill, fill = c.head_dim > 128 ? all / 2 : all;
   int64_t shares = fill / c.num_kv_heads, most = busy * (context / p.slots) / kFp4MinSteps;
   if (shares > most) shares = most;
+  const bool uneven = busy * c.num_kv_heads < (few ? 4 * fill : fill);
   p.busy = busy;
-  p.shares = busy * c.num_kv_heads < 4 * fill && shares > busy / 4 ? (int32_t)shares : 0;
+  p.shares = uneven && shares > (few ? busy / 4 : busy) ? (int32_t)shares : 0;
   return p;
 }
 

@@ -100,10 +100,13 @@ class Case4(A.Case):
     def planes(self):
         return as_planes(self.cache.numpy(), self.layout)
 
-    def set_scale(self, r, slot, head, w, group, byte):
-        """One group's scale byte of request r's slot."""
+    def set_scale(self, r, slot, head, w, group, byte, code=None):
+        """One group's scale byte of request r's slot, and all its codes."""
         n = self.block * self.dim // 2
         b = self.table[r, slot // self.block]
+        if code is not None:
+            at = slot % self.block * self.dim // 2 + group * 16
+            self.planes()[b, head, w, at:at + 16] = code | code << 4
         self.planes()[b, head, w, n + slot % self.block * (self.dim // 32) + group] = byte
 
     def rows_of(self, r):

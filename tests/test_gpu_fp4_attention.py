@@ -150,13 +150,14 @@ def test_strided_rows_no_lse_and_struct():
 @pytest.mark.parametrize("dim", [64, 256])
 @pytest.mark.parametrize("lens", [[(1, 200), (1, 31)], [(6, 200), (3, 31)], [(150, 200), (33, 40)]])
 def test_nan_and_infinite_slots_reach_only_rows_that_see_them(lens, dim, dtype):
-    """NaN scales of K and V, and scales of V whose values are infinite in the type, in slots that some rows do not see."""
+    """NaN scales of K and V, and infinite values of V, in slots that some rows do not see. (Values that are finite but near
+    the end of 32 bits' range are another matter: 2^8 times as much is summed up before it is divided.)"""
     case = F.Case4(12, lens, heads=4, kv_heads=2, dim=dim, dtype=dtype)
     n = lens[0][0]
     case.set_scale(0, 200 - n, 0, 1, 0, 255)     # the first new token's own V: all new tokens see it
     case.set_scale(0, 199, 0, 0, dim // 32 - 1, 255)  # the last one's K
-    case.set_scale(0, 10, 1, 1, 1, 254)          # outside the window of most
-    case.set_scale(0, 199, 1, 1, 0, 253)
+    case.set_scale(0, 10, 1, 1, 1, 254, 7)          # outside the window of most
+    case.set_scale(0, 199, 1, 1, 0, 253, 14)
     case.set_scale(1, 30, 1, 1, dim // 32 - 1, 255)
     for causal, window in ((True, 0), (True, 20), (False, 7)):
         run(case, causal=causal, window=window)
