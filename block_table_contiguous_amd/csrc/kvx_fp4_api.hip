@@ -52,8 +52,12 @@ kvx_status check_transfer(const kvx_paged_cache* c, const kvx_fp4_cache* b, int3
   if (num_layers < 0 || total_blocks < 0 || total_blocks > kInt32Max || c->block_size != b->block_size ||
       c->head_dim != b->head_dim || c->num_kv_heads != b->num_kv_heads || c->dtype != b->dtype ||
       (int64_t)num_layers * total_blocks > b->num_blocks ||
-      (int64_t)c->block_size * (c->head_dim / KVX_FP4_GROUP) > kInt32Max / (2 * c->num_kv_heads))  // groups of a block
+      // a block's groups of 32 elements are numbered in 32 bits
+      (int64_t)c->block_size * (c->head_dim / KVX_FP4_GROUP) > kInt32Max / (2 * c->num_kv_heads))
     return KVX_ERR_INVALID_ARGUMENT;
+  // so are the pieces of 128 of them of a layer, of which a launch takes 16 a workgroup
+  const int64_t pieces = ((int64_t)c->block_size * (c->head_dim / KVX_FP4_GROUP) * 2 * c->num_kv_heads + 127) / 128;
+  if (total_blocks > (1 << 27) / pieces) return KVX_ERR_INVALID_ARGUMENT;
   return st;
 }
 

@@ -151,6 +151,7 @@ __device__ __forceinline__ int64_t find_run(const kvx_xfer* xfers, int64_t count
 struct Groups {
   Divisor per_plane, per_row;  // groups of a plane and of a row
   uint32_t of_block;           // groups
+  Divisor pieces;              // wavefronts' shares of a block
 };
 struct Place {
   uint32_t head, w, row, at, in_row;  // at: in the plane
@@ -160,70 +161,209 @@ __device__ __forceinline__ Place place(const Groups& g, uint32_t i) {
   return {plane >> 1, plane & 1, row, at, at - row * g.per_row.by};
 }
 
-// A wavefront's block: its layer's cache at the block, and the 4-bit block; false if there is none.
-struct Pair {
-  char* wide;
-  char* narrow;
-};
-template <bool PACK>
-__device__ __forceinline__ bool find_pair(const Fp4CopyArgs& a, int64_t item, int lane, Pair* at) {
-  const int64_t l = item / a.total_blocks, p = item - l * a.total_blocks;
-  int64_t count = *a.xfer_count;
-  if (count > a.total_blocks) count = a.total_blocks;
-  if (count <= 0) return false;
-  const int64_t k = find_run(a.xfers, count, p, lane);
-  if (k < 0) return false;
-  const kvx_xfer x = a.xfers[k];
-  if (p - x.buf_block >= x.num_blocks) return false;
-  const int64_t id = (PACK ? x.src_block : x.dst_block) + (p - x.buf_block);
-  if (id < 0 || id >= a.cache.num_blocks) {
-    if (lane == 0) raise(a.err, KVX_DEVERR_BLOCK_RANGE);
-    return false;
-  }
-  at->wide = (char*)a.layer_bases[l] + id * a.cache.block_stride_bytes;
-  at->narrow = (char*)a.buffer.base + item * a.buffer.block_stride_bytes;
-  return true;
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  return (int64_t)(uint32_t)uniform((int32_t)x) | (int64_t)uniform((int32_t)(x >> 32)) << 32;
 }
 
-// Four lanes a group, eight elements each.
-template <class E, bool PACK>
-__global__ __launch_bounds__(kCopyThreads) void copy_fp4_kernel(Fp4CopyArgs a, Groups g) {
-  const int lane = threadIdx.x & 63;
-  const int dim = a.cache.head_dim, c = lane & 3;
-  const int64_t items = a.num_layers * a.total_blocks;
-  for (int64_t item = (int64_t)blockIdx.x * (kCopyThreads / 64) + threadIdx.x / 64; item < items;
-       item += (int64_t)gridDim.x * (kCopyThreads / 64)) {
-  Pair to;
-  if (!find_pair<PACK>(a, item, lane, &to)) continue;
-  for (uint32_t i = lane >> 2; i < g.of_block; i += 16) {
-    const Place x = place(g, i);
-    char* wide = to.wide + x.row * a.cache.token_stride_bytes + x.w * a.cache.kv_stride_bytes +
-                 x.head * a.cache.head_stride_bytes + x.in_row * (kGroup * 2) + c * 16;
-    char* plane = to.narrow + x.head * a.buffer.head_stride_bytes + x.w * a.buffer.kv_stride_bytes;
-    char* codes = plane + x.at * (kGroup / 2) + c * 4;
-    char* scale = plane + a.cache.block_size * (dim / 2) + x.at;
-    if constexpr (PACK) {
-      const f32x8 v = widen<E>(gload<u32x4>(wide));
-      const uint32_t s = scale_byte<E>(top_of_quad(top_of(v)));
-      gstore(codes, encode(v, s));
-      if (c == 0) gstore(scale, (uint8_t)s);
-    } else {
-      gstore(wide, decode<E>(gload<uint32_t>(codes), scale_of(gload<uint8_t>(scale))));
+// The runs of a wavefront's blocks, one after another. Runs, counts and bases come by the scalar unit: vector loads would queue
+// behind the data.
+template <class T>
+__device__ __forceinline__ T constant(const T* p) {
+  return *(const __attribute__((address_space(4))) T*)p;
+}
+template <bool PACK>
+struct Runs {
+  const Fp4CopyArgs& a;
+  int64_t count, k;   // runs, and the present one
+  int64_t from, to;   // its blocks of the buffer
+  int64_t id;         // cache block of the first
+  char* base;         // of the layer
+  __device__ __forceinline__ Runs(const Fp4CopyArgs& args, int l, uint32_t p, int lane) : a(args) {
+    count = constant(a.xfer_count);
+    if (count > a.total_blocks) count = a.total_blocks;
+    base = (char*)constant(a.layer_bases + l);
+    k = count > 0 ? uniform(find_run(a.xfers, count, p, lane)) : -1;
+    if (k < 0) k = 0;
+    read();
+  }
+  __device__ __forceinline__ void read() {
+    from = to = INT64_MAX;
+    if (k >= count) return;
+    from = constant(&a.xfers[k].buf_block);
+    to = from + constant(&a.xfers[k].num_blocks);
+    id = PACK ? constant(&a.xfers[k].src_block) : constant(&a.xfers[k].dst_block);
+  }
+  // The cache's block for block p of the buffer, p not falling; NULL if there is none.
+  __device__ __forceinline__ char* block(uint32_t p, int lane) {
+    while (p >= to) {
+      ++k;
+      read();
+    }
+    if (p < from) return nullptr;
+    const int64_t at = id + (p - from);
+    if (at < 0 || at >= a.cache.num_blocks) {
+      if (lane == 0) raise(a.err, KVX_DEVERR_BLOCK_RANGE);
+      return nullptr;
+    }
+    return base + at * a.cache.block_stride_bytes;
+  }
+};
+
+// Data that is read and written once goes past the caches.
+template <class T>
+__device__ __forceinline__ T gload_once(const void* p) {
+  return __builtin_nontemporal_load((const __attribute__((address_space(1))) T*)p);
+}
+template <class T>
+__device__ __forceinline__ void gstore_once(void* p, T v) {
+  __builtin_nontemporal_store(v, (__attribute__((address_space(1))) T*)p);
+}
+
+// The 4x4 words of four neighbouring lanes transposed: lane c ends with the c-th word of each.
+__device__ __forceinline__ u32x4 transposed(u32x4 v, int c) {
+  auto swap = [](uint32_t& low, uint32_t& high, bool upper, auto dpp) {
+    const uint32_t got = dpp(upper ? low : high);
+    if (upper) low = got;
+    else high = got;
+  };
+  uint32_t a = v[0], b = v[1], d = v[2], e = v[3];
+  auto by1 = [](uint32_t x) -> uint32_t { return __builtin_amdgcn_mov_dpp(x, 0xb1, 0xf, 0xf, true); };
+  auto by2 = [](uint32_t x) -> uint32_t { return __builtin_amdgcn_mov_dpp(x, 0x4e, 0xf, 0xf, true); };
+  swap(a, b, c & 1, by1);
+  swap(d, e, c & 1, by1);
+  swap(a, d, c & 2, by2);
+  swap(b, e, c & 2, by2);
+  return {a, b, d, e};
+}
+template <int I>
+__device__ __forceinline__ uint32_t of_lane(uint32_t x) {  // of the four neighbours
+  return __builtin_amdgcn_mov_dpp(x, I * 0x55, 0xf, 0xf, true);
+}
+
+// A wavefront takes 128 groups at a time, 8 KiB of the 16-bit side, and kPieces such pieces one after another, the next one's loads
+// before the present one's stores. On the 16-bit side four lanes hold a group, 16 bytes each; on the 4-bit side a lane holds one, and words
+// change lanes between the two, so that both move 1 KiB an instruction. Bound by HBM bytes, read and written once.
+//   EVEN, where rows are 1, 2, 4 or 8 groups and planes whole times 16: 16 groups are rows of one plane, whose place the scalar
+//   unit finds; a lane's place among them never changes.
+constexpr int kPiece = 128, kLoads = kPiece / 16, kPieces = 2;
+template <class E, bool PACK, bool EVEN>
+__global__ __launch_bounds__(kCopyThreads) void copy_fp4_kernel(Fp4CopyArgs a, Groups g, uint32_t pieces) {
+  const int lane = threadIdx.x & 63, c = lane & 3, quad = lane >> 2;
+  const int64_t scales = (int64_t)a.cache.block_size * (a.cache.head_dim / 2);
+  const uint32_t my_row = quad / g.per_row;
+  const int64_t my_wide = my_row * a.cache.token_stride_bytes + (quad - my_row * g.per_row.by) * (kGroup * 2) + c * 16;
+  constexpr int NV = PACK ? kLoads : kLoads / 4;
+  struct Piece {
+    char* cache;   // the cache's block; NULL: none
+    char* buffer;  // and the buffer's
+    uint32_t first;
+    u32x4 v[NV];
+    uint32_t s[NV];
+  };
+  // the 16-bit side of group first + i * 16 + quad, or NULL behind the block's last
+  auto wide = [&](const Piece& x, int i) -> char* {
+    const uint32_t at = x.first + i * 16 + (EVEN ? 0 : quad);
+    if (at >= g.of_block) return nullptr;
+    const Place y = place(g, at);
+    char* p = x.cache + y.row * a.cache.token_stride_bytes + y.w * a.cache.kv_stride_bytes + y.head * a.cache.head_stride_bytes;
+    return EVEN ? p + my_wide : p + y.in_row * (kGroup * 2) + c * 16;
+  };
+  // the 4-bit side of group first + (i + c) * 16 + quad, i a multiple of 4
+  auto narrow = [&](const Piece& x, int i, char** scale) -> char* {
+    const uint32_t at = x.first + (i + c) * 16 + quad;
+    if (at >= g.of_block) return nullptr;
+    const Place y = place(g, at);
+    char* plane = x.buffer + y.head * a.buffer.head_stride_bytes + y.w * a.buffer.kv_stride_bytes;
+    *scale = plane + scales + y.at;
+    return plane + (int64_t)y.at * (kGroup / 2);
+  };
+  auto load = [&](Piece& x) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      char* scale;
+      const char* p = PACK ? wide(x, i) : narrow(x, i * 4, &scale);
+      x.v[i] = u32x4{0, 0, 0, 0};
+      x.s[i] = 0;
+      if (p) {
+        x.v[i] = gload_once<u32x4>(p);
+        if (!PACK) x.s[i] = gload_once<uint8_t>(scale);
+      }
+    }
+  };
+  auto store = [&](const Piece& x) {
+#pragma unroll
+    for (int i = 0; i < kLoads; i += 4) {
+      if constexpr (PACK) {
+        u32x4 codes;
+        uint32_t s[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const f32x8 y = widen<E>(x.v[i + k]);
+          s[k] = scale_byte<E>(top_of_quad(top_of(y)));
+          codes[k] = encode(y, s[k]);
+        }
+        codes = transposed(codes, c);
+        char* scale;
+        char* p = narrow(x, i, &scale);
+        if (!p) continue;
+        gstore_once(p, codes);
+        gstore(scale, (uint8_t)(c & 2 ? (c & 1 ? s[3] : s[2]) : (c & 1 ? s[1] : s[0])));
+      } else {
+        const u32x4 codes = transposed(x.v[i / 4], c);
+        const uint32_t s = x.s[i / 4], of[4] = {of_lane<0>(s), of_lane<1>(s), of_lane<2>(s), of_lane<3>(s)};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          char* p = wide(x, i + k);
+          if (p) gstore_once(p, decode<E>(codes[k], scale_of(of[k])));
+        }
+      }
+    }
+  };
+  const uint32_t share = blockIdx.x * (kCopyThreads / 64) + uniform((int32_t)(threadIdx.x / 64));
+  for (int l = blockIdx.y; l < a.num_layers; l += gridDim.y) {
+    if (share >= (pieces + kPieces - 1) / kPieces) break;
+    const uint32_t begin = share * kPieces, end = begin + kPieces < pieces ? begin + kPieces : pieces;
+    Runs<PACK> runs(a, l, begin / g.pieces, lane);
+    auto find = [&](Piece& x, uint32_t i) {
+      const uint32_t block = i / g.pieces;
+      x.first = (i - block * g.pieces.by) * kPiece;
+      x.cache = runs.block(block, lane);
+      x.buffer = (char*)a.buffer.base + (l * a.total_blocks + block) * a.buffer.block_stride_bytes;
+      if (x.cache) load(x);
+    };
+    Piece now, next;
+    find(now, begin);
+    for (uint32_t i = begin; i < end; ++i) {
+      next.cache = nullptr;
+      if (i + 1 < end) find(next, i + 1);
+      if (now.cache) store(now);
+      now = next;
     }
   }
-  }
+}
+
+template <class E, bool PACK>
+void launch_copy_type(const Fp4CopyArgs& a, const Groups& g, uint32_t pieces, dim3 grid, hipStream_t stream) {
+  if (16 % g.per_row.by == 0 && g.per_plane.by % 16 == 0)
+    copy_fp4_kernel<E, PACK, true><<<grid, kCopyThreads, 0, stream>>>(a, g, pieces);
+  else copy_fp4_kernel<E, PACK, false><<<grid, kCopyThreads, 0, stream>>>(a, g, pieces);
 }
 
 template <bool PACK>
 hipError_t launch_copy(const Fp4CopyArgs& a, hipStream_t stream) {
   const uint32_t row = a.cache.head_dim / kGroup, plane = row * a.cache.block_size;
-  const uint32_t of_block = plane * 2 * a.cache.num_kv_heads;
-  const Groups g = {divisor(plane), divisor(row), of_block};
-  const int64_t items = a.num_layers * a.total_blocks, per = kCopyThreads / 64;
-  const int64_t groups = (items + per - 1) / per, most = (1 << 24) - 1;  // a launch has fewer than 2^32 threads
-  const dim3 grid((unsigned)(groups < most ? groups : most));
-  if (a.cache.dtype == KVX_DTYPE_BF16) copy_fp4_kernel<Bf16, PACK><<<grid, kCopyThreads, 0, stream>>>(a, g);
-  else copy_fp4_kernel<Fp16, PACK><<<grid, kCopyThreads, 0, stream>>>(a, g);
+  const uint32_t of_block = plane * 2 * a.cache.num_kv_heads, in_block = (of_block + kPiece - 1) / kPiece;
+  const Groups g = {divisor(plane), divisor(row), of_block, divisor(in_block)};
+  // a layer's pieces by column, and layers by row; a launch has fewer than 2^32 threads, layers beyond are taken in turn
+  const int64_t pieces = a.total_blocks * in_block, per = kPieces * (kCopyThreads / 64);
+  const int64_t columns = (pieces + per - 1) / per;
+  int64_t rows = ((1 << 24) - 1) / columns;
+  if (rows > a.num_layers) rows = a.num_layers;
+  if (rows > 65535) rows = 65535;
+  const dim3 grid((unsigned)columns, (unsigned)rows);
+  if (a.cache.dtype == KVX_DTYPE_BF16) launch_copy_type<Bf16, PACK>(a, g, (uint32_t)pieces, grid, stream);
+  else launch_copy_type<Fp16, PACK>(a, g, (uint32_t)pieces, grid, stream);
   return hipGetLastError();
 }
 
