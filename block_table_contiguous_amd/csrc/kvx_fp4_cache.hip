@@ -12,6 +12,17 @@ namespace {
 // the write of rotated new rows
 // --------------------------------------------------------------------------------------
 
+// Data that is read, or written, once goes past the caches (9461 tokens of 32 + 8 heads rotated and written: 57 us with the caches'
+// default policy for the loads, 48 so).
+template <class T>
+__device__ __forceinline__ T gload_once(const void* p) {
+  return __builtin_nontemporal_load((const __attribute__((address_space(1))) T*)p);
+}
+template <class T>
+__device__ __forceinline__ void gstore_once(void* p, T v) {
+  __builtin_nontemporal_store(v, (__attribute__((address_space(1))) T*)p);
+}
+
 constexpr int kRopeThreads = 256;
 
 // A 64-bit number to 32 bits so that a later rounding to fewer bits is as if it were the only one: toward zero, with the
@@ -21,26 +32,61 @@ __device__ __forceinline__ float sticky(double x) {
   return (float)__builtin_bit_cast(double, (b ^ low) | (low ? 0x20000000ull : 0));
 }
 
-// One workgroup a token. Its first rot_dim/2 threads form the angles' cosines and sines once, in 64 bits: a rotated key is rounded
-// to 4 bits, and 32 bits on the way there would decide some of the elements next to a border between two codes.
-// The rows of q are then moved as 16-byte vectors, turned in 32 bits; of K and V four neighbouring lanes hold a group
-// of 32 elements, eight each, with the partners of the eight read beside them.
+// One workgroup a token. Its first rot_dim/2 threads form the angles' cosines and sines, once for all heads and in 64 bits: a rotated
+// key is rounded to 4 bits, and 32 bits on the way there would decide some of the elements next to a border between two codes.
+// Rows are moved as 16-byte vectors, the first on their way while the angles are formed and the next while a thread turns its own: of K
+// and V four neighbouring lanes hold a group of 32 elements, eight each, with the partners of the eight beside them; of q a thread holds
+// whole pairs. Bound by HBM bytes for many tokens, by a launch and the chain positions, angles, stores for a few.
+struct RopeUnits {
+  Divisor of_head, of_q_head;  // vectors of a K or V head, units of a q head
+  int32_t kv, all;             // vectors of K and V, and all units
+};
+struct Unit {
+  u32x4 a, b;
+  int32_t head, at;  // at: vector of the head, or unit of a q head
+  int32_t kind;      // 1: K, 2: V, 3: q
+};
 template <class E, bool INTERLEAVED>
-__global__ __launch_bounds__(kRopeThreads) void rope_fp4_kernel(Fp4RopeArgs a, BlockDiv div) {
+__global__ __launch_bounds__(kRopeThreads) void rope_fp4_kernel(Fp4RopeArgs a, BlockDiv div, RopeUnits n) {
   __shared__ double turn[KVX_MAX_HEAD_DIM];  // cos of pair i, then sin
+  __shared__ float turn32[KVX_MAX_HEAD_DIM];
   const int64_t t = blockIdx.x;
-  const int half = a.rot_dim / 2, dim = a.cache.head_dim, vecs = dim / 8;
+  const int half = a.rot_dim / 2, dim = a.cache.head_dim;
   const kvx_fp4_cache& cache = a.cache;
+  const int rot_units = INTERLEAVED ? a.rot_dim / 8 : a.rot_dim / 16;
+  auto q_offset = [&](int c) { return c < rot_units ? c * 16 : a.rot_dim * 2 + (c - rot_units) * 16; };
+  auto load = [&](int u, Unit* x) {
+    if (u < n.kv) {
+      const int h2 = (uint32_t)u / n.of_head, heads = cache.num_kv_heads;
+      const bool is_v = h2 >= heads;
+      x->kind = is_v ? 2 : 1;
+      x->head = is_v ? h2 - heads : h2;
+      x->at = u - h2 * n.of_head.by;
+      const RowView& in = is_v ? a.value : a.key;
+      const char* src = in.base + t * in.token_stride + x->head * in.head_stride + x->at * 16;
+      x->a = gload_once<u32x4>(src);
+      if (!INTERLEAVED && !is_v && x->at * 8 < a.rot_dim) x->b = gload_once<u32x4>(src + (x->at * 8 < half ? half * 2 : -half * 2));
+    } else {
+      x->kind = 3;
+      x->head = (uint32_t)(u - n.kv) / n.of_q_head;
+      x->at = u - n.kv - x->head * n.of_q_head.by;
+      const char* src = a.query.base + t * a.query.token_stride + x->head * a.query.head_stride + q_offset(x->at);
+      x->a = gload_once<u32x4>(src);
+      if (!INTERLEAVED && x->at < rot_units) x->b = gload_once<u32x4>(src + half * 2);
+    }
+  };
+  Unit x;
+  if (threadIdx.x < n.all) load(threadIdx.x, &x);
   const int64_t slot = a.slots[t];
   char* block = nullptr;  // of the slot; NULL: none
-  int row = 0;
+  int64_t row = 0;
   if (slot >= 0) {
     const int64_t b = slot / div.size;
     if (b >= cache.num_blocks) {
       if (threadIdx.x == 0) raise(a.err, KVX_DEVERR_SLOT_RANGE);
     } else {
       block = (char*)cache.base + b * cache.block_stride_bytes;
-      row = (int)(slot - b * div.size);
+      row = slot - b * div.size;
     }
   }
   for (int i = threadIdx.x; i < half; i += kRopeThreads) {
@@ -50,80 +96,73 @@ __global__ __launch_bounds__(kRopeThreads) void rope_fp4_kernel(Fp4RopeArgs a, B
     sincospi(2.0 * (turns - rint(turns)), &s, &c);
     turn[i] = c;
     turn[half + i] = s;
+    turn32[i] = (float)c;
+    turn32[half + i] = (float)s;
   }
   __syncthreads();
 
-  // query rows: a vector of whole pairs, a pair of vectors half a rotation apart, or a vector that passes through
-  const int rot_units = INTERLEAVED ? a.rot_dim / 8 : a.rot_dim / 16, head_units = rot_units + (dim - a.rot_dim) / 8;
-  for (int u = threadIdx.x; u < a.num_heads * head_units; u += kRopeThreads) {
-    const int h = u / head_units, c = u - h * head_units;
-    const char* src = a.query.base + t * a.query.token_stride + h * a.query.head_stride;
-    char* dst = (char*)a.out.base + t * a.out.token_stride + h * a.out.head_stride;
-    const int off = c < rot_units ? c * 16 : a.rot_dim * 2 + (c - rot_units) * 16;
-    const u32x4 first = gload<u32x4>(src + off);
-    if (c >= rot_units) {
-      gstore(dst + off, first);
-    } else if constexpr (INTERLEAVED) {
-      f32x8 v = widen<E>(first);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float cs = (float)turn[c * 4 + j], sn = (float)turn[half + c * 4 + j];
-        const float p = v[2 * j], q = v[2 * j + 1];
-        v[2 * j] = p * cs - q * sn;
-        v[2 * j + 1] = q * cs + p * sn;
-      }
-      gstore(dst + off, narrow<E>(v));
-    } else {
-      f32x8 p = widen<E>(first), q = widen<E>(gload<u32x4>(src + half * 2 + off));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float cs = (float)turn[c * 8 + j], sn = (float)turn[half + c * 8 + j];
-        const float x = p[j], y = q[j];
-        p[j] = x * cs - y * sn;
-        q[j] = y * cs + x * sn;
-      }
-      gstore(dst + off, narrow<E>(p));
-      gstore(dst + half * 2 + off, narrow<E>(q));
-    }
-  }
-
-  // K, then V; a wavefront's lanes beyond the last vector are whole groups of four
-  if (!block && !a.key_out.base) return;
-  const int per = cache.num_kv_heads * vecs;
-  for (int u = threadIdx.x; u < 2 * per; u += kRopeThreads) {
-    const bool is_v = u >= per;
-    const int y = is_v ? u - per : u, h = y / vecs, c = y - h * vecs;
-    const RowView& in = is_v ? a.value : a.key;
-    const char* src = in.base + t * in.token_stride + h * in.head_stride;
-    f32x8 v = widen<E>(gload<u32x4>(src + c * 16));
-    if (!is_v && c * 8 < a.rot_dim) {
-      if constexpr (INTERLEAVED) {
+  for (int u = threadIdx.x; u < n.all; u += kRopeThreads) {
+    const Unit y = x;
+    if (u + kRopeThreads < n.all) load(u + kRopeThreads, &x);
+    if (y.kind == 3) {
+      char* dst = (char*)a.out.base + t * a.out.token_stride + y.head * a.out.head_stride + q_offset(y.at);
+      if (y.at >= rot_units) {
+        gstore(dst, y.a);
+      } else if constexpr (INTERLEAVED) {
+        f32x8 v = widen<E>(y.a);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const double cs = turn[c * 4 + j], sn = turn[half + c * 4 + j], p = v[2 * j], q = v[2 * j + 1];
-          v[2 * j] = sticky(p * cs - q * sn);
-          v[2 * j + 1] = sticky(q * cs + p * sn);
+          const float cs = turn32[y.at * 4 + j], sn = turn32[half + y.at * 4 + j];
+          const float p = v[2 * j], q = v[2 * j + 1];
+          v[2 * j] = p * cs - q * sn;
+          v[2 * j + 1] = q * cs + p * sn;
         }
+        gstore(dst, narrow<E>(v));
       } else {
-        const bool second = c * 8 >= half;
-        const int pair = second ? c * 8 - half : c * 8;
-        const f32x8 o = widen<E>(gload<u32x4>(src + c * 16 + (second ? -half * 2 : half * 2)));
+        f32x8 p = widen<E>(y.a), q = widen<E>(y.b);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const double cs = turn[pair + j], sn = second ? turn[half + pair + j] : -turn[half + pair + j];
-          v[j] = sticky((double)v[j] * cs + (double)o[j] * sn);
+          const float cs = turn32[y.at * 8 + j], sn = turn32[half + y.at * 8 + j];
+          const float v = p[j], w = q[j];
+          p[j] = v * cs - w * sn;
+          q[j] = w * cs + v * sn;
+        }
+        gstore(dst, narrow<E>(p));
+        gstore(dst + half * 2, narrow<E>(q));
+      }
+    } else {
+      f32x8 v = widen<E>(y.a);
+      const int at = y.at * 8;
+      if (y.kind == 1 && at < a.rot_dim) {
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const double cs = turn[y.at * 4 + j], sn = turn[half + y.at * 4 + j], p = v[2 * j], q = v[2 * j + 1];
+            v[2 * j] = sticky(p * cs - q * sn);
+            v[2 * j + 1] = sticky(q * cs + p * sn);
+          }
+        } else {
+          const bool second = at >= half;
+          const int pair = second ? at - half : at;
+          const f32x8 o = widen<E>(y.b);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const double cs = turn[pair + j], sn = second ? turn[half + pair + j] : -turn[half + pair + j];
+            v[j] = sticky((double)v[j] * cs + (double)o[j] * sn);
+          }
         }
       }
-    }
-    const uint32_t s = scale_byte<E>(top_of_quad(top_of(v))), codes = encode(v, s);
-    if (block) {
-      char* plane = block + h * cache.head_stride_bytes + (is_v ? cache.kv_stride_bytes : 0);
-      gstore(plane + row * (dim / 2) + c * 4, codes);
-      if (c % 4 == 0) gstore(plane + cache.block_size * (dim / 2) + row * (dim / kGroup) + c / 4, (uint8_t)s);
-    }
-    if (a.key_out.base) {
-      const RowView& o = is_v ? a.value_out : a.key_out;
-      gstore((char*)o.base + t * o.token_stride + h * o.head_stride + c * 16, decode<E>(codes, scale_of(s)));
+      const uint32_t s = scale_byte<E>(top_of_quad(top_of(v))), codes = encode(v, s);
+      if (block) {
+        char* plane = block + y.head * cache.head_stride_bytes + (y.kind == 2 ? cache.kv_stride_bytes : 0);
+        gstore(plane + row * (dim / 2) + y.at * 4, codes);
+        if (y.at % 4 == 0)
+          gstore(plane + (int64_t)cache.block_size * (dim / 2) + row * (dim / kGroup) + y.at / 4, (uint8_t)s);
+      }
+      if (a.key_out.base) {
+        const RowView& o = y.kind == 2 ? a.value_out : a.key_out;
+        gstore((char*)o.base + t * o.token_stride + y.head * o.head_stride + y.at * 16, decode<E>(codes, scale_of(s)));
+      }
     }
   }
 }
@@ -209,16 +248,6 @@ struct Runs {
     return base + at * a.cache.block_stride_bytes;
   }
 };
-
-// Data that is read and written once goes past the caches.
-template <class T>
-__device__ __forceinline__ T gload_once(const void* p) {
-  return __builtin_nontemporal_load((const __attribute__((address_space(1))) T*)p);
-}
-template <class T>
-__device__ __forceinline__ void gstore_once(void* p, T v) {
-  __builtin_nontemporal_store(v, (__attribute__((address_space(1))) T*)p);
-}
 
 // The 4x4 words of four neighbouring lanes transposed: lane c ends with the c-th word of each.
 __device__ __forceinline__ u32x4 transposed(u32x4 v, int c) {
@@ -372,12 +401,15 @@ hipError_t launch_copy(const Fp4CopyArgs& a, hipStream_t stream) {
 hipError_t launch_rope_fp4(const Fp4RopeArgs& a, bool interleaved, hipStream_t stream) {
   const dim3 grid((unsigned)a.num_tokens), block(kRopeThreads);
   const BlockDiv div = block_div(a.cache.block_size);
+  const int32_t vecs = a.cache.head_dim / 8, kv = 2 * a.cache.num_kv_heads * vecs;
+  const int32_t q_head = (interleaved ? a.rot_dim / 8 : a.rot_dim / 16) + (a.cache.head_dim - a.rot_dim) / 8;
+  const RopeUnits n = {divisor(vecs), divisor(q_head), kv, kv + a.num_heads * q_head};
   if (a.cache.dtype == KVX_DTYPE_BF16) {
-    if (interleaved) rope_fp4_kernel<Bf16, true><<<grid, block, 0, stream>>>(a, div);
-    else rope_fp4_kernel<Bf16, false><<<grid, block, 0, stream>>>(a, div);
+    if (interleaved) rope_fp4_kernel<Bf16, true><<<grid, block, 0, stream>>>(a, div, n);
+    else rope_fp4_kernel<Bf16, false><<<grid, block, 0, stream>>>(a, div, n);
   } else {
-    if (interleaved) rope_fp4_kernel<Fp16, true><<<grid, block, 0, stream>>>(a, div);
-    else rope_fp4_kernel<Fp16, false><<<grid, block, 0, stream>>>(a, div);
+    if (interleaved) rope_fp4_kernel<Fp16, true><<<grid, block, 0, stream>>>(a, div, n);
+    else rope_fp4_kernel<Fp16, false><<<grid, block, 0, stream>>>(a, div, n);
   }
   return hipGetLastError();
 }
