@@ -121,11 +121,12 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
   return a / b;
 }
-template <int ROWS, int BN>
+// EXTRA: steps that stand for a tile's start, before its own, where a share that meets several tiles should get less of them.
+template <int ROWS, int BN, int EXTRA = 0>
 __device__ __forceinline__ void extent(const AttendArgs& a, const Rows& x, int group, int32_t* tiles, int32_t* steps) {
   *tiles = (int32_t)(((int64_t)x.tokens * group + ROWS - 1) / ROWS);
   const int lo = sees(a, x, 0).x, hi = sees(a, x, x.tokens - 1).y;
-  *steps = hi > lo ? (hi + BN - 1) / BN - lo / BN : 1;
+  *steps = (hi > lo ? (hi + BN - 1) / BN - lo / BN : 1) + EXTRA;
 }
 // 64 requests of the batch, one a lane: their tiles and steps, and those of all requests before them. Offsets that
 // give the same rows to many requests can make more tiles than 32 bits hold: tile0 then wraps around, and who takes a
@@ -136,13 +137,13 @@ struct Requests {
   uint32_t tile0;
   int64_t step0;
 };
-template <int ROWS, int BN>
+template <int ROWS, int BN, int EXTRA>
 __device__ __forceinline__ Requests sixty_four(const AttendArgs& a, int group, int64_t cap, int lane, int r0, uint32_t tile0,
                                                int64_t step0) {
   Requests q = {};
   if (r0 + lane < a.batch.num_reqs) {
     q.x = request(a, r0 + lane, cap);
-    extent<ROWS, BN>(a, q.x, group, &q.tiles, &q.steps);
+    extent<ROWS, BN, EXTRA>(a, q.x, group, &q.tiles, &q.steps);
   }
   int64_t sum = (int64_t)q.tiles * q.steps;
   uint32_t num = q.tiles;
@@ -158,13 +159,13 @@ __device__ __forceinline__ Requests sixty_four(const AttendArgs& a, int group, i
 }
 // Counts the steps of the batch, and finds the request for which holds(shares, a lane's request) is
 // true: its lane's values in every lane, steps == 0 where there is none.
-template <int ROWS, int BN, class F>
+template <int ROWS, int BN, int EXTRA = 0, class F>
 __device__ __forceinline__ Requests locate(const AttendArgs& a, int group, int64_t cap, int lane, int shares, Shares* all,
                                            F holds) {
   Requests q = {};
   const int reqs = a.batch.num_reqs;
   for (int r0 = 0; r0 < reqs; r0 += 64)
-    q = sixty_four<ROWS, BN>(a, group, cap, lane, r0, lane_of((int32_t)(q.tile0 + q.tiles), 63),
+    q = sixty_four<ROWS, BN, EXTRA>(a, group, cap, lane, r0, lane_of((int32_t)(q.tile0 + q.tiles), 63),
                              lane_of(q.step0 + (int64_t)q.tiles * q.steps, 63));
   all->steps = lane_of(q.step0 + (int64_t)q.tiles * q.steps, 63);
   all->count = all->steps < shares ? (int32_t)all->steps : shares;
@@ -174,7 +175,7 @@ __device__ __forceinline__ Requests locate(const AttendArgs& a, int group, int64
   Requests f = q;
   for (int r0 = 0;; r0 += 64) {
     if (reqs > 64)  // up to 64 requests the first pass holds them all
-      f = sixty_four<ROWS, BN>(a, group, cap, lane, r0, r0 ? lane_of((int32_t)(f.tile0 + f.tiles), 63) : 0,
+      f = sixty_four<ROWS, BN, EXTRA>(a, group, cap, lane, r0, r0 ? lane_of((int32_t)(f.tile0 + f.tiles), 63) : 0,
                                r0 ? lane_of(f.step0 + (int64_t)f.tiles * f.steps, 63) : 0);
     const uint64_t there = __ballot(f.tiles > 0 && holds(*all, f));
     if (there) {
@@ -278,7 +279,7 @@ struct Split {
 // Joins the parts of a tile: out = sum_s 2^(lse_s - top) o_s / sum_s 2^(lse_s - top). A thread takes four
 // dimensions of one row, and with many parts only every second or eighth of them, the threads of a row and
 // dimension side by side. What bounds it is one chain of loads: the batch, then the parts.
-template <class E, int ROWS, int BN>
+template <class E, int ROWS, int BN, int EXTRA = 0>
 __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, Split sp) {
   __shared__ f32x4 sums[256];
   __shared__ float tops[256], totals[256];
@@ -287,7 +288,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttendArgs a, Split sp) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int g = blockIdx.x % a.cache.num_kv_heads, tile = blockIdx.x / a.cache.num_kv_heads;
   Shares all;
-  const Requests q = locate<ROWS, BN>(a, group, cap, lane, sp.shares, &all, [&](const Shares&, const Requests& q) {
+  const Requests q = locate<ROWS, BN, EXTRA>(a, group, cap, lane, sp.shares, &all, [&](const Shares&, const Requests& q) {
     return tile - q.tile0 < (uint32_t)q.tiles;
   });
   if (q.steps == 0) return;  // no such tile

@@ -65,14 +65,15 @@ __device__ __forceinline__ f32x4 decode4(uint32_t codes, float scale) {
 // One pass over the slots with a running maximum and sum, scores transposed (S^T = K q^T), so that a lane holds one query
 // row and four slots of each 16, and the weights are where O^T += V^T P^T takes them. RT tiles of 16 rows are the same for the
 // four wavefronts of a workgroup, which take 32 slots each of every 128 and meet only at the end. A lane loads whole groups of 32
-// elements with their scales. Of K, widened to 16 bits, they are the matrix unit's operand as they stand, because the summed dimension
+// elements (of heads of up to 64, half groups) with their scales. Of K, widened to 16 bits, they are the matrix unit's operand as they stand, because the summed dimension
 // may be numbered in any order; V goes widened to LDS and is read from there with the transposing load. DP is head_dim padded to 64, 128 or 256.
 //   SHARED: the grid's workgroups take equal shares of the whole batch's steps (see Shares).
 template <class E, int DP, int RT, bool SHARED>
-__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(AttendArgs args, BlockDiv div, Split sp) {
+__global__ __launch_bounds__(256, DP > 128 ? 3 - RT : 4 - RT) void attend_fp4_kernel(AttendArgs args, BlockDiv div, Split sp) {
   const AttendArgs a = argument<AttendArgs>();
   constexpr int ROWS = 16 * RT, KW = 32, BN = 4 * KW, KT = KW / 16;
   constexpr int KS = DP > 128 ? 2 : 1, DT = DP / 16;
+  constexpr int W = DP > 64 ? 4 : 2;  // words of a row that a lane loads at a time: a piece
   constexpr int VROW = DP * 2 + 32;  // bytes of a row of V in LDS
   constexpr int TILE = 4 * KW * VROW, JOIN = 4 * 16 * DP * 4;
   __shared__ __align__(16) char smem[TILE > JOIN ? TILE : JOIN];
@@ -80,7 +81,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(Atte
 
   const int tid = threadIdx.x, lane = tid & 63, w = uniform((int32_t)(tid >> 6));
   const int n = lane & 15, hq = lane >> 4;
-  const int group = a.num_heads / a.cache.num_kv_heads, dim = a.cache.head_dim, groups = dim / kGroup;
+  const int group = a.num_heads / a.cache.num_kv_heads, dim = a.cache.head_dim, groups = dim / kGroup, pieces = dim / (W * 8);
   const int64_t cap = a.batch.max_blocks_per_req * a.cache.block_size;
   int g = blockIdx.x % a.cache.num_kv_heads, index = blockIdx.x / a.cache.num_kv_heads;
   if constexpr (SHARED) {  // shares that follow one another to one XCD: workgroup i runs on XCD i % 8
@@ -92,7 +93,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(Atte
   if (blockIdx.x == 0) check_batch(a, cap, tid, 256);
 
   char* const own = smem + w * KW * VROW;  // this wavefront's rows of V
-  char* const put = own + n * VROW + hq * 64;
+  char* const put = own + n * VROW + hq * (W * 16);
   const char* const get = own + (4 * hq + (n >> 2)) * VROW + (n & 3) * 8;
 
   Rows x;
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(Atte
   uint32_t tile0 = 0;
   int64_t left = 1;
   if constexpr (SHARED) {
-    const Requests q = locate<ROWS, BN>(a, group, cap, lane, sp.shares, &all, [&](const Shares& s, const Requests& q) {
+    const Requests q = locate<ROWS, BN, kFp4Extra>(a, group, cap, lane, sp.shares, &all, [&](const Shares& s, const Requests& q) {
       const int64_t begin = share_begin(s, index);
       return index < s.count && q.step0 <= begin && begin < q.step0 + (int64_t)q.tiles * q.steps;
     });
@@ -118,7 +119,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(Atte
     x = find_rows<ROWS>(a, sp.tiles - 1 - index, group, cap, lane);
     if (x.tile < 0 || (int64_t)x.tile * ROWS >= (int64_t)x.tokens * group) return;
   }
-  int errs = 0;
+  bool bad_blocks = false;
   for (;;) {
   if constexpr (SHARED) {
     if (tile0 + x.tile >= (uint32_t)sp.tiles) break;  // offsets that are not a CSR: the workspace has no slots for more
@@ -147,29 +148,31 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(Atte
   const int t_first = first.x / BN, t_all = (kend + BN - 1) / BN - t_first;
   int tb = t_first, te = t_first + (t_all > 0 ? t_all : 0);
   if constexpr (SHARED) {
-    if (t_all == steps) {
-      tb = t_first + from;
-      te = t_first + to;
+    // the first kFp4Extra steps of a tile stand for its start
+    const int own = steps - kFp4Extra, b = from > kFp4Extra ? from - kFp4Extra : 0, e = to > kFp4Extra ? to - kFp4Extra : 0;
+    if (t_all == own) {
+      tb = t_first + b;
+      te = t_first + e;
     } else {  // a tile whose rows see less than all of the request's: its steps in proportion
       const int64_t mine = te - tb;
-      te = tb + (int)quotient(mine * to, steps);
-      tb = tb + (int)quotient(mine * from, steps);
+      te = tb + (int)quotient(mine * e, own);
+      tb = tb + (int)quotient(mine * b, own);
     }
   }
   tb = uniform(tb);
   te = uniform(te);
 
-  // q: lane 16 g + n has group g (and g + 4) of row n, as it will have of K
-  u32x4 q[RT][KS][4];
+  // q: lane 16 g + n has piece g (and g + 4) of row n, as it will have of K
+  u32x4 q[RT][KS][W];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const char* p = a.query.base + q_row[rt] * a.query.token_stride + head[rt] * a.query.head_stride;
 #pragma unroll
     for (int c = 0; c < KS; ++c)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < W; ++k) {
         q[rt][c][k] = u32x4{0, 0, 0, 0};
-        if (used[rt] && c * 4 + hq < groups) q[rt][c][k] = gload<u32x4>(p + (c * 4 + hq) * (kGroup * 2) + k * 16);
+        if (used[rt] && c * 4 + hq < pieces) q[rt][c][k] = gload<u32x4>(p + (c * 4 + hq) * (W * 16) + k * 16);
       }
   }
 
@@ -189,55 +192,51 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(Atte
   }
   const float c1 = a.scale * kLog2e;
 
-  // Lane 16 g + n of a wavefront stages group g (and g + 4) of slots n and 16 + n of its 32. A slot that is not there is read
-  // from the cache's first rows; its scale of V becomes 0 and its weight is.
+  // Lane 16 g + n of a wavefront stages piece g (and g + 4) of slots n and 16 + n of its 32. A slot that is not there is read
+  // from the cache's first rows; its scale of V becomes 0 and its weight is. Lanes past a narrower head's last piece load that
+  // one again: q is zero there, and such columns of V reach no element of the result.
+  typedef uint32_t Words __attribute__((ext_vector_type(W)));
+  struct {
+    Words k[KT][KS], v[KT][KS];
+    uint32_t ks[KT][KS], vs[KT][KS];
+    uint32_t there;  // one bit a slot
+  } in;
+  uint32_t at[KS];
+#pragma unroll
+  for (int c = 0; c < KS; ++c) at[c] = c * 4 + hq < pieces ? c * 4 + hq : pieces - 1;
   int32_t ids[KT];
-  auto load_ids = [&](int t) {
+  auto load_ids = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < KT; ++i) {
       const int b = block_of(div, t * BN + w * KW + i * 16 + n);
       ids[i] = gload<int32_t>(table + (b < cols ? b : cols - 1));
     }
   };
-  u32x4 rk[KT][KS], rv[KT][KS];
-  uint32_t ks[KT][KS], vs[KT][KS];
-  uint32_t there = 0;
-  auto fetch = [&](int t) {
-    there = 0;
+  auto fetch = [&](int t) __attribute__((always_inline)) {
+    in.there = 0;
 #pragma unroll
     for (int i = 0; i < KT; ++i) {
       const int j = t * BN + w * KW + i * 16 + n;
-      const bool in = j < kend, ok = in && (uint32_t)ids[i] < (uint64_t)a.cache.num_blocks;
-      if (in && !ok) errs |= KVX_DEVERR_BLOCK_RANGE;
-      there |= (uint32_t)(__ballot(ok) & 0xffff) << (16 * i);
-      const int o = j - block_of(div, j) * div.size;
+      const bool wanted = j < kend, ok = wanted && (uint32_t)ids[i] < (uint64_t)a.cache.num_blocks;
+      bad_blocks |= wanted && !ok;
+      in.there |= (uint32_t)(__ballot(ok) & 0xffff) << (16 * i);
+      const int64_t o = ok ? j - block_of(div, j) * div.size : 0;
       const char* k = base + (ok ? ids[i] * a.cache.block_stride_bytes : 0);
-      const char* e = k + (ok ? o : 0) * (dim / 2);
-      const char* s = k + scales + (ok ? o : 0) * groups;
+      const char* e = k + o * (dim / 2);
+      const char* s = k + scales + o * groups;
 #pragma unroll
       for (int c = 0; c < KS; ++c) {
-        const int at = c * 4 + hq;
-        rk[i][c] = rv[i][c] = u32x4{0, 0, 0, 0};
-        ks[i][c] = vs[i][c] = 0;
-        if (at < groups) {
-          rk[i][c] = gload<u32x4>(e + at * 16);
-          ks[i][c] = gload<uint8_t>(s + at);
-          rv[i][c] = gload<u32x4>(e + at * 16 + a.cache.kv_stride_bytes);
-          vs[i][c] = gload<uint8_t>(s + at + a.cache.kv_stride_bytes);
-        }
+        in.k[i][c] = gload<Words>(e + at[c] * (W * 4));
+        in.ks[i][c] = gload<uint8_t>(s + at[c] * W / 4);
+        in.v[i][c] = gload<Words>(e + a.cache.kv_stride_bytes + at[c] * (W * 4));
+        in.vs[i][c] = gload<uint8_t>(s + a.cache.kv_stride_bytes + at[c] * W / 4);
       }
     }
   };
-
-  if (tb < te) {
-    load_ids(tb);
-    fetch(tb);
-    load_ids(tb + 1);
-  }
-  for (int t = tb; t < te; ++t) {
+  bool far = false;  // some row's scores are (see is_far)
+  auto step = [&](int t) __attribute__((always_inline)) {
     const int k0 = t * BN + w * KW;
     const bool inner = t * BN >= last.x && t * BN + BN <= first.y;
-    const uint32_t here_mask = there;
     f32x4 s[RT][KT];
 #pragma unroll
     for (int i = 0; i < KT; ++i) {
@@ -245,37 +244,40 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(Atte
       for (int rt = 0; rt < RT; ++rt) s[rt][i] = f32x4{};
 #pragma unroll
       for (int c = 0; c < KS; ++c) {
-        const float scale = scale_of(ks[i][c]);
+        const float scale = scale_of(in.ks[i][c]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const u32x4 wide = decode<E>(rk[i][c][k], scale);
+        for (int k = 0; k < W; ++k) {
+          const u32x4 wide = decode<E>(in.k[i][c][k], scale);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) s[rt][i] = product(E(), wide, q[rt][c][k], s[rt][i]);
         }
       }
     }
-    // A weight of zero times a NaN or infinity is NaN: groups of V that may read back as one are left out of the products
+    // A weight of zero times a NaN or infinity is NaN: pieces of V that may read back as one are left out of the products
     // and added below for the rows that see them.
     uint64_t odd[KT][KS], any_odd = 0;
+    if (!inner || in.there != 0xffffffffu) {
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+          if (!(in.there >> (16 * i + n) & 1)) in.vs[i][c] = 0;
+          const bool bad = in.vs[i][c] > kFiniteScales<E> && c * 4 + hq < pieces;
+          any_odd |= odd[i][c] = __ballot(bad);
+          if (in.vs[i][c] > kFiniteScales<E>) in.vs[i][c] = 0, in.v[i][c] = Words(0);
+        }
+    }
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
       for (int c = 0; c < KS; ++c) {
-        odd[i][c] = 0;
-        if (!(here_mask >> (16 * i + n) & 1)) vs[i][c] = 0;
-        if (!inner) {
-          const bool bad = vs[i][c] > kFiniteScales<E>;
-          any_odd |= odd[i][c] = __ballot(bad);
-          if (bad) vs[i][c] = 0, rv[i][c] = u32x4{0, 0, 0, 0};
-        }
-        const float scale = scale_of(vs[i][c]);
+        const float scale = scale_of(in.vs[i][c]);
         char* at = put + i * 16 * VROW + c * 256;
-        if (DP >= 128 || hq * 32 < DP) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) *(u32x4*)(at + k * 16) = decode<E>(rv[i][c][k], scale);
-        }
+        for (int k = 0; k < W; ++k) *(u32x4*)(at + k * 16) = decode<E>(in.v[i][c][k], scale);
       }
     __builtin_amdgcn_wave_barrier();
+    const uint32_t there = in.there;
     if (t + 1 < te) {
       fetch(t + 1);
       load_ids(t + 2);
@@ -284,9 +286,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(Atte
     u32x4 p[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      if (!inner || here_mask != 0xffffffffu) {
+      if (!inner || there != 0xffffffffu) {
         const int at = k0 + 4 * hq, lo = see[rt].x - at, hi = see[rt].y - at;
-        const uint32_t mine = here_mask >> (4 * hq);
+        const uint32_t mine = there >> (4 * hq);
 #pragma unroll
         for (int i = 0; i < KT; ++i)
 #pragma unroll
@@ -302,7 +304,6 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(Atte
         for (int r = 0; r < 4; ++r) top = fmaxf(top, s[rt][i][r]);
       top = max_over_rows(top) * c1;
       // the reference moves only when the maximum leaves its range: the sums keep their 32 bits
-      bool far = false;
       if (__any(top > m[rt] + (kLift<E> + kLag<E>))) {
         const float held = m[rt];
         const float to = top - held > kLift<E> + kLag<E> ? (is_far(top) ? top : top - kLift<E>) : held;
@@ -311,20 +312,23 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(Atte
         l[rt] *= shrink;
 #pragma unroll
         for (int d = 0; d < DT; ++d) acc[rt][d] *= shrink;
+        far |= __any(is_far(to));
       }
-      far = __any(is_far(m[rt]));
       const float ref = m[rt] == -INFINITY ? 0.0f : m[rt];
       f32x8 pv;
+      if (far) {  // rounded before the reference is taken from it, as the maximum was
 #pragma unroll
-      for (int i = 0; i < KT; ++i)
+        for (int i = 0; i < KT * 4; ++i) pv[i] = rounded_difference(rounded_product(s[rt][i / 4][i % 4], c1), ref);
+      } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float v = s[rt][i][r];
-          // far: rounded before the reference is taken from it, as the maximum was
-          const float e = far ? rounded_difference(rounded_product(v, c1), ref) : __builtin_fmaf(v, c1, -ref);
-          l[rt] += pv[4 * i + r] = __builtin_amdgcn_exp2f(e);
-          s[rt][i][r] = pv[4 * i + r];
-        }
+        for (int i = 0; i < KT * 4; ++i) pv[i] = __builtin_fmaf(s[rt][i / 4][i % 4], c1, -ref);
+      }
+#pragma unroll
+      for (int i = 0; i < KT * 4; ++i) {
+        pv[i] = __builtin_amdgcn_exp2f(pv[i]);
+        l[rt] += pv[i];
+        s[rt][i / 4][i % 4] = pv[i];
+      }
       p[rt] = narrow<E>(pv);  // one rounding of each weight to the element type, which the matrix unit takes
     }
 #pragma unroll
@@ -345,8 +349,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(Atte
             const int from = __builtin_ctzll(todo), o = from & 15, at = c * 4 + (from >> 4), j = k0 + i * 16 + o;
             const int b = block_of(div, j);
             const char* plane = base + table[b] * a.cache.block_stride_bytes + a.cache.kv_stride_bytes;
-            const int in = j - b * div.size;
-            const float scale = scale_of(gload<uint8_t>(plane + scales + in * groups + at));
+            const int64_t row = j - b * div.size;
+            const float scale = scale_of(gload<uint8_t>(plane + scales + row * groups + at * W / 4));
+            const uint32_t parts = W == 4 ? 3u << (2 * at) : 1u << at;  // a bit each, so that no index into the sums is made of it
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
               const float mine = o % 4 == 0 ? s[rt][i][0] : o % 4 == 1 ? s[rt][i][1] : o % 4 == 2 ? s[rt][i][2] : s[rt][i][3];
@@ -354,15 +359,23 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(Atte
               if (j < see[rt].x || j >= see[rt].y) continue;
 #pragma unroll
               for (int d = 0; d < DT; ++d) {
-                if (d >> 1 != at) continue;
-                const uint32_t codes = gload<uint16_t>(plane + in * (dim / 2) + d * 8 + 2 * hq);
+                if (!(parts >> d & 1)) continue;
+                const uint32_t codes = gload<uint16_t>(plane + row * (dim / 2) + d * 8 + 2 * hq);
                 acc[rt][d] += pj * decode4<E>(codes, scale);
               }
             }
           }
     }
     __builtin_amdgcn_wave_barrier();
+  };
+
+  // a step's loads go out while the one before forms its weights, the block ids a step ahead of them
+  if (tb < te) {
+    load_ids(tb);
+    fetch(tb);
+    load_ids(tb + 1);
   }
+  for (int t = tb; t < te; ++t) step(t);
 
   // join the wavefronts: weights of each one's sum, then the sums themselves through LDS
   const AttendArgs end = argument<AttendArgs>();
@@ -425,13 +438,13 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_kernel(Atte
     tile0 += tiles;
     do {
       x = request_uniform(a, x.r + 1, cap);
-      extent<ROWS, BN>(a, x, group, &tiles, &steps);
+      extent<ROWS, BN, kFp4Extra>(a, x, group, &tiles, &steps);
       tiles = uniform(tiles);
       steps = uniform(steps);
     } while (tiles == 0);
   }
   }
-  if (errs) raise(a.err, errs);
+  if (bad_blocks) raise(a.err, KVX_DEVERR_BLOCK_RANGE);
 }
 
 // In the 32x32x16 products lane l holds column (or row) l % 32 and, with hf = l / 32, elements 8 hf to 8 hf + 7 of the summed
@@ -861,10 +874,10 @@ void launch_attend(const AttendArgs& a, BlockDiv div, const Split& sp, int rows,
   const dim3 join((unsigned)blocks, (unsigned)several);
   if (rows == 16) {
     attend_fp4_kernel<E, DP, 1, true><<<grid, 256, 0, stream>>>(a, div, sp);
-    join_kernel<E, 16, 128><<<join, 256, 0, stream>>>(a, sp);
+    join_kernel<E, 16, 128, kFp4Extra><<<join, 256, 0, stream>>>(a, sp);
   } else if (rows == 32) {
     attend_fp4_kernel<E, DP, 2, true><<<grid, 256, 0, stream>>>(a, div, sp);
-    join_kernel<E, 32, 128><<<join, 256, 0, stream>>>(a, sp);
+    join_kernel<E, 32, 128, kFp4Extra><<<join, 256, 0, stream>>>(a, sp);
   } else {
     if (by_block) attend_fp4_rows_kernel<E, DP, true, true><<<grid, 256, 0, stream>>>(a, div, sp);
     else attend_fp4_rows_kernel<E, DP, false, true><<<grid, 256, 0, stream>>>(a, div, sp);

@@ -207,10 +207,6 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
 
 // The runs of a wavefront's blocks, one after another. Runs, counts and bases come by the scalar unit: vector loads would queue
 // behind the data.
-template <class T>
-__device__ __forceinline__ T constant(const T* p) {
-  return *(const __attribute__((address_space(4))) T*)p;
-}
 template <bool PACK>
 struct Runs {
   const Fp4CopyArgs& a;

@@ -23,11 +23,8 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
   return s < 0 ? 0 : s > most ? most : s;
 }
 
-// 2^(s - 127) as the conversions take it.
-__device__ __forceinline__ float scale_of(uint32_t s) {
-  const uint32_t bits = s << 23;
-  return __builtin_bit_cast(float, bits > 0x400000u ? bits : 0x400000u);
-}
+// 2^(s - 127) as the conversions take it: the exponent's bits, and one below them so that s = 0 is no zero and s = 255 is NaN.
+__device__ __forceinline__ float scale_of(uint32_t s) { return __builtin_bit_cast(float, s << 23 | 0x400000u); }
 
 // Eight elements to their codes, the first in the lowest bits.
 __device__ __forceinline__ uint32_t encode(f32x8 v, uint32_t s) {
@@ -75,6 +72,12 @@ __device__ __forceinline__ uint32_t top_of_quad(uint32_t x) {
   x = x > y ? x : y;
   y = __builtin_amdgcn_mov_dpp(x, 0x4e, 0xf, 0xf, true);  // lanes 2 3 0 1
   return x > y ? x : y;
+}
+
+// What no kernel writes while this one runs and all lanes ask for: a scalar load.
+template <class T>
+__device__ __forceinline__ T constant(const T* p) {
+  return *(const __attribute__((address_space(4))) T*)p;
 }
 
 // Division of 32-bit numbers by one that the host knows: a product, a sum and shifts.
