@@ -93,8 +93,11 @@ __global__ __launch_bounds__(256, DP > 128 ? 3 - RT : 4 - RT) void attend_fp4_ke
   if (blockIdx.x == 0) check_batch(a, cap, tid, 256);
 
   char* const own = smem + w * KW * VROW;  // this wavefront's rows of V
-  char* const put = own + n * VROW + hq * (W * 16);
-  const char* const get = own + (4 * hq + (n >> 2)) * VROW + (n & 3) * 8;
+  // the 16-byte pieces of every second four rows change places in pairs, so that eight rows' writes of one, which go out
+  // together, fall on different 16 bytes of 128
+  const int odd_row = (n >> 2 & 1) * 16;
+  char* const put[2] = {own + n * VROW + hq * (W * 16) + odd_row, own + n * VROW + hq * (W * 16) - odd_row};
+  const char* const get = own + (4 * hq + (n >> 2)) * VROW + ((((n >> 1) & 1) ^ (hq & 1)) * 16) + (n & 1) * 8;
 
   Rows x;
   Shares all;
@@ -272,9 +275,8 @@ __global__ __launch_bounds__(256, DP > 128 ? 3 - RT : 4 - RT) void attend_fp4_ke
 #pragma unroll
       for (int c = 0; c < KS; ++c) {
         const float scale = scale_of(in.vs[i][c]);
-        char* at = put + i * 16 * VROW + c * 256;
 #pragma unroll
-        for (int k = 0; k < W; ++k) *(u32x4*)(at + k * 16) = decode<E>(in.v[i][c][k], scale);
+        for (int k = 0; k < W; ++k) *(u32x4*)(put[k & 1] + i * 16 * VROW + c * 256 + k * 16) = decode<E>(in.v[i][c][k], scale);
       }
     __builtin_amdgcn_wave_barrier();
     const uint32_t there = in.there;
@@ -487,9 +489,12 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_rows_kernel
   // lane 16 q + s stages group q (and q + 4) of slot s of its wavefront's 16
   const int slot = lane & 15, quarter = lane >> 4;
   char* const sk_put = sk + (w * KW + slot) * KROW + quarter * 64;
-  char* const sv_put = sv + (w * KW + slot) * VROW + quarter * 64;
+  // The 16-byte pieces of a row's groups in V change places by row: piece i of row r is at i ^ (r / 2 % 4). Eight lanes write at a
+  // time, eight rows' pieces, which then fall on different 16 bytes of 128; unchanged, they take four times as long.
+  const uint32_t sv_put = BN * KROW + (w * KW + slot) * VROW + quarter * 64 + (slot >> 1 & 3) * 16;
   const char* const sk_get = sk + n * KROW + hf * 16;
-  const char* const sv_get = sv + (4 * hf + ((lane & 15) >> 2)) * VROW + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+  const int of_row = 4 * hf + ((lane & 15) >> 2), piece = ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1);
+  const char* const sv_get = sv + of_row * VROW + (piece ^ (of_row >> 1 & 3)) * 16 + (lane & 1) * 8;
 
   Rows x;
   Shares all;
@@ -664,7 +669,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_rows_kernel
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           *(u32x4*)(sk_put + c * 256 + k * 16) = decode<E>(rk[c][k], k_scale);
-          *(u32x4*)(sv_put + c * 256 + k * 16) = decode<E>(rv[c][k], v_scale);
+          *(u32x4*)(smem + ((sv_put + c * 256) ^ (k * 16))) = decode<E>(rv[c][k], v_scale);
         }
       }
     }

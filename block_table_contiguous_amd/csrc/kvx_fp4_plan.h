@@ -9,8 +9,8 @@ namespace kvx {
 
 // A request's rows of one KV head are taken 16 or 32 at a time, by four wavefronts that take 32 slots each of every 128, or, where there
 // are more, 128 at a time, 64 slots a step. Where the tiles do not fill the GPU, or a decode batch's contexts are uneven, the
-// batch's steps are shared out evenly (see Shares) to as many workgroups as the GPU holds, of kFp4MinSteps steps at least.
-constexpr int kFp4MinSteps = 4;
+// batch's steps are shared out evenly (see Shares) to as many workgroups as the GPU holds, of 256 slots at least (with 512, one request of 8000 slots takes 18.1 us
+// and not 16.1).
 constexpr int kFp4Extra = 2;  // steps of 128 slots that the start of a tile of few rows counts for
 constexpr int64_t kFp4MaxWorkgroups = (1 << 24) - 1;  // of 256 threads: a launch has fewer than 2^32
 
@@ -33,10 +33,12 @@ inline Fp4Plan plan_attention_fp4(const kvx_paged_cache& c, const kvx_batch& b, 
   if (busy > p.tiles) busy = p.tiles;
   if (busy < 1) busy = 1;
   const int64_t context = b.max_context_len < 0x7fffffff ? b.max_context_len : 0x7fffffff;
-  // The workgroups that the registers leave room for, 1 to 3 a CU. With 768 instead, 32 requests of up to 8192 slots, 32 heads on 8, one
-  // token of dimension 256 take 158 us and not 82, 8 tokens of 128 84 and not 66; with 512 one token of 128 46 and not 38.
-  const int fill = c.head_dim > 128 ? (p.rows == 16 ? 512 : 256) : (p.rows == 16 ? 768 : 512);
-  int64_t shares = fill / c.num_kv_heads, most = busy * (context / p.slots) / kFp4MinSteps;
+  // The workgroups that the registers leave room for, 1 to 4 a CU. 32 requests of up to 8192 slots, 32 heads on 8: one token of
+  // dimension 256 takes 82 us, with 768 158; 8 tokens of 128 66 us, with 768 84; one of 128 38 us, with 512 46 and with 1024 49; one of
+  // 64 34 us, with 768 36.
+  const int dim = c.head_dim;
+  const int fill = p.rows == 16 ? (dim > 128 ? 512 : dim > 64 ? 768 : 1024) : dim > 128 ? 256 : few && dim <= 64 ? 768 : 512;
+  int64_t shares = fill / c.num_kv_heads, most = busy * (context / 256);
   if (shares > most) shares = most;
   const bool uneven = busy * c.num_kv_heads < (few ? 4 * fill : fill);
   p.busy = busy;

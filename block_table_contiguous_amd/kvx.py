@@ -935,7 +935,7 @@ def fp4_cache(kv_cache, head_dim: int, dtype, layout: str = "blocks_heads_kv") -
         raise ValueError("kvx: the planes of a 4-bit cache must be dense")
     # a plane grows by more than its padding with every token, so its size says how many there are
     tokens = shape[3] * FP4_GROUP // (17 * head_dim) if head_dim > 0 else 0
-    if tokens < 1 or fp4_plane_bytes(tokens, head_dim) != shape[3]:
+    if tokens < 1 or head_dim % FP4_GROUP or (tokens * 17 * head_dim // FP4_GROUP + 15) // 16 * 16 != shape[3]:
         raise ValueError("kvx: the last dimension of a 4-bit cache must be fp4_plane_bytes(block_size, head_dim)")
     # the stride of a dimension with one entry is never used and may be anything
     c = Fp4Cache(kv_cache.data_ptr(), shape[b], stride[b] if shape[b] > 1 else 0, stride[w],
