@@ -890,6 +890,29 @@ def kvx_evict_compact(kv_cache, block_table, dst_block_table, keep, mass=None, m
 # calls on a paged cache held in 4 bits (include/kvx_fp4.h)
 # ---------------------------------------------------------------------------------------
 
+# A decode step makes two of these calls a layer: the usual tensors, dense ones, are told by one comparison each, and the module is
+# imported once.
+
+_torch = None
+
+
+def _th():
+    global _torch
+    if _torch is None:
+        import torch
+
+        _torch = torch
+    return _torch
+
+
+def _dense_rows(t, tokens: int, heads: int, dtype, cache: "Fp4Cache", name: str):
+    """_rows, with a short way for dense [tokens][heads][head_dim] of the cache's type (dtype)."""
+    dim = cache.head_dim
+    if t.dtype is dtype and t.is_contiguous() and t.shape == (tokens, heads, dim):
+        return 2 * heads * dim, 2 * dim
+    return _rows(t, tokens, heads, cache, name)
+
+
 _FP4_AXES = {"blocks_heads_kv": (0, 1, 2), "blocks_kv_heads": (0, 2, 1), "kv_blocks_heads": (1, 2, 0)}  # blocks, heads, K/V
 
 
@@ -923,23 +946,22 @@ def fp4_cache(kv_cache, head_dim: int, dtype, layout: str = "blocks_heads_kv") -
     struct that the calls below take, for rows of head_dim elements and calls whose other rows are
     of dtype. They make it from the tensor themselves; a caller that makes the same call many times
     can make it once and pass it instead."""
-    import torch
-
-    shape, stride = kv_cache.shape, kv_cache.stride()
-    if layout not in _FP4_AXES:
+    shape, stride, axes = kv_cache.shape, kv_cache.stride(), _FP4_AXES.get(layout)
+    if axes is None:
         raise ValueError(f"unknown layout {layout}")
-    b, h, w = _FP4_AXES[layout]
-    if kv_cache.dtype != torch.uint8 or len(shape) != 4 or shape[w] != 2:
+    b, h, w = axes
+    if kv_cache.dtype is not _th().uint8 or len(shape) != 4 or shape[w] != 2:
         raise ValueError("kvx: a 4-bit cache is a 4-D uint8 tensor of the given layout")
     if stride[3] != 1:
         raise ValueError("kvx: the planes of a 4-bit cache must be dense")
+    blocks, heads, plane = shape[b], shape[h], shape[3]
     # a plane grows by more than its padding with every token, so its size says how many there are
-    tokens = shape[3] * FP4_GROUP // (17 * head_dim) if head_dim > 0 else 0
-    if tokens < 1 or head_dim % FP4_GROUP or (tokens * 17 * head_dim // FP4_GROUP + 15) // 16 * 16 != shape[3]:
+    tokens = plane * FP4_GROUP // (17 * head_dim) if head_dim > 0 else 0
+    if tokens < 1 or head_dim % FP4_GROUP or (tokens * 17 * head_dim // FP4_GROUP + 15) // 16 * 16 != plane:
         raise ValueError("kvx: the last dimension of a 4-bit cache must be fp4_plane_bytes(block_size, head_dim)")
     # the stride of a dimension with one entry is never used and may be anything
-    c = Fp4Cache(kv_cache.data_ptr(), shape[b], stride[b] if shape[b] > 1 else 0, stride[w],
-                 stride[h] if shape[h] > 1 else 0, tokens, shape[h], head_dim, _dtype_code(dtype, "dtype"))
+    c = Fp4Cache(kv_cache.data_ptr(), blocks, stride[b] if blocks > 1 else 0, stride[w], stride[h] if heads > 1 else 0, tokens,
+                 heads, head_dim, _dtype_code(dtype, "dtype"))
     c.tensor = kv_cache  # kept alive, and looked at for its device
     return c
 
@@ -959,8 +981,7 @@ def kvx_rope_and_cache_fp4(query, key, value, positions, inv_freq, pair_axis: Se
     """kvx_rope_and_cache into a 4-bit cache (a tensor of new_fp4_cache's layouts, or fp4_cache of
     it). key_out and value_out ([num_tokens][num_kv_heads][head_dim], both or neither) get what the
     cache then holds of each token; they must not overlap key and value."""
-    import torch
-
+    torch = _th()
     c = _fp4(kv_cache, key, layout)
     _want(slot_mapping, torch.int64, "slot_mapping")
     _want(positions, torch.int64, "positions")
@@ -976,18 +997,21 @@ def kvx_rope_and_cache_fp4(query, key, value, positions, inv_freq, pair_axis: Se
         raise ValueError("kvx: query and query_out go together")
     if (key_out is None) != (value_out is None):
         raise ValueError("kvx: key_out and value_out go together")
-    ks = _rows(key, T, c.num_kv_heads, c, "key")
-    vs = _rows(value, T, c.num_kv_heads, c, "value")
+    kv, dtype = c.num_kv_heads, key.dtype
+    if _dtype_code(dtype, "key") != c.dtype:
+        raise TypeError("kvx: key and the cache must have the same element type")
+    ks = _dense_rows(key, T, kv, dtype, c, "key")
+    vs = _dense_rows(value, T, kv, dtype, c, "value")
     heads, qs, os_, q_ptr, o_ptr = 0, (0, 0), (0, 0), None, None
     if query is not None:
-        qs = _rows(query, T, None, c, "query")
-        heads = query.shape[1]
-        os_ = _rows(query_out, T, heads, c, "query_out")
+        heads = query.shape[1] if query.dim() == 3 else 0
+        qs = _dense_rows(query, T, heads, dtype, c, "query")
+        os_ = _dense_rows(query_out, T, heads, dtype, c, "query_out")
         q_ptr, o_ptr = query.data_ptr(), query_out.data_ptr()
     kos, vos, ko_ptr, vo_ptr = (0, 0), (0, 0), None, None
     if key_out is not None:
-        kos = _rows(key_out, T, c.num_kv_heads, c, "key_out")
-        vos = _rows(value_out, T, c.num_kv_heads, c, "value_out")
+        kos = _dense_rows(key_out, T, kv, dtype, c, "key_out")
+        vos = _dense_rows(value_out, T, kv, dtype, c, "value_out")
         ko_ptr, vo_ptr = key_out.data_ptr(), value_out.data_ptr()
     _on_current_device((query, key, value, positions, inv_freq, slot_mapping, c.tensor, query_out, key_out, value_out,
                         err_flag))
@@ -1027,7 +1051,7 @@ def kvx_paged_attention_fp4(query, kv_cache, block_table, q_offsets, context_len
     it), with a workspace of new_attention_workspace_fp4."""
     c = _fp4(kv_cache, query, layout)
     b, heads, qs = _batch(query, c, block_table, q_offsets, context_lens, max_query_len, max_context_len)
-    os_ = _rows(out, b.num_tokens, heads, c, "out")
+    os_ = _dense_rows(out, b.num_tokens, heads, query.dtype, c, "out")
     if lse is not None:
         _want_lse(lse, b.num_tokens, heads)
     nbytes = 0
@@ -1045,8 +1069,7 @@ def kvx_paged_attention_fp4(query, kv_cache, block_table, q_offsets, context_len
 def _transfer_fp4(layer_bases, kv_cache, xfers, xfer_count, total_blocks: int, buffer, layout, buffer_layout,
                   err_flag):
     """(cache, buffer) structs of a transfer between 16-bit layers like kv_cache and 4-bit blocks."""
-    import torch
-
+    torch = _th()
     c = _cache(kv_cache, layout)
     f = buffer if type(buffer) is Fp4Cache else fp4_cache(
         buffer, c.head_dim, torch.bfloat16 if c.dtype == DTYPE_BF16 else torch.float16, buffer_layout)

@@ -201,6 +201,13 @@ def test_binding_refuses_what_the_abi_cannot_see():
         a.update(kw)
         with pytest.raises(ValueError):
             K.kvx_rope_and_cache_fp4(**a)
+    for kw in (dict(kv_cache=c), dict(value=k.half()), dict(query=q.half()), dict(query_out=out.half()), dict(key_out=k.half(), value_out=k),
+               dict(key=k.float(), kv_cache=K.fp4_cache(kv, 64, torch.bfloat16))):
+        a = dict(query=q, key=k, value=k, positions=pos, inv_freq=freq, pair_axis=[0] * 32, slot_mapping=slots, kv_cache=kv,
+                 query_out=out)
+        a.update(kw)
+        with pytest.raises(TypeError):
+            K.kvx_rope_and_cache_fp4(**a)
     layer = torch.zeros(9, 16, 2, 2, 64, dtype=torch.bfloat16)
     runs, count = torch.zeros(4, 4, dtype=torch.int64), torch.zeros(1, dtype=torch.int64)
     bases = torch.zeros(2, dtype=torch.int64)
