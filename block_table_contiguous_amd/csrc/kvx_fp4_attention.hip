@@ -197,7 +197,7 @@ __global__ __launch_bounds__(256, DP > 128 ? 3 - RT : 4 - RT) void attend_fp4_ke
 
   // Lane 16 g + n of a wavefront stages piece g (and g + 4) of slots n and 16 + n of its 32. A slot that is not there is read
   // from the cache's first rows; its scale of V becomes 0 and its weight is. Lanes past a narrower head's last piece load that
-  // one again: q is zero there, and such columns of V reach no element of the result.
+  // one again: q is zero there and K's scale 1, and such columns of V reach no element of the result.
   typedef uint32_t Words __attribute__((ext_vector_type(W)));
   struct {
     Words k[KT][KS], v[KT][KS];
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(256, DP > 128 ? 3 - RT : 4 - RT) void attend_fp4_ke
       for (int rt = 0; rt < RT; ++rt) s[rt][i] = f32x4{};
 #pragma unroll
       for (int c = 0; c < KS; ++c) {
-        const float scale = scale_of(in.ks[i][c]);
+        const float scale = c * 4 + hq < pieces ? scale_of(in.ks[i][c]) : 1.0f;
 #pragma unroll
         for (int k = 0; k < W; ++k) {
           const u32x4 wide = decode<E>(in.k[i][c][k], scale);

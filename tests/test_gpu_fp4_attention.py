@@ -164,6 +164,25 @@ def test_nan_and_infinite_slots_reach_only_rows_that_see_them(lens, dim, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim", [32, 96, 160, 224])
+@pytest.mark.parametrize("lens", [[(1, 200)], [(6, 200)], [(150, 200)]])
+def test_infinite_keys_on_the_far_side(lens, dim, dtype):
+    """A key that reads back infinite, with a score of minus infinity: its slot weighs nothing, as with one whose score is
+    merely far below the others', and heads narrower than the kernels' widths see no infinity times zero."""
+    case = F.Case4(13, lens, heads=4, kv_heads=2, dim=dim, dtype=dtype)
+    case.q[:, :, :32] = -case.q[:, :, :32].abs() - 0.25
+    case.q[:, :, -32:] = -case.q[:, :, -32:].abs() - 0.25
+    outs = []
+    for byte in (254 if dtype == "bf16" else 150, 138):  # 6 * 2^127 and 6 * 2^23 are infinite in the types, 6 * 2^11 is not
+        for head, group in ((0, 0), (1, dim // 32 - 1)):
+            case.set_scale(0, 10, head, 0, group, byte, 7)
+        outs.append(F.attend(case, case.to()))
+    run(case)
+    for inf, low in zip(*outs):
+        assert inf == low if isinstance(inf, int) else torch.equal(inf, low)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_small_and_large_scales(dtype):
     """K groups near the ends of the scale's range beside ordinary ones; V as far as the type goes."""
     case = F.Case4(13, [(1, 100), (20, 60)], heads=4, kv_heads=2, dim=64, dtype=dtype)
