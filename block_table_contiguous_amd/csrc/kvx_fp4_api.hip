@@ -55,9 +55,9 @@ kvx_status check_transfer(const kvx_paged_cache* c, const kvx_fp4_cache* b, int3
       // a block's groups of 32 elements are numbered in 32 bits
       (int64_t)c->block_size * (c->head_dim / KVX_FP4_GROUP) > kInt32Max / (2 * c->num_kv_heads))
     return KVX_ERR_INVALID_ARGUMENT;
-  // so are the pieces of 128 of them of a layer, of which a launch takes 16 a workgroup
+  // so are the pieces of 128 of them of a layer, of which a workgroup of 256 threads takes 8: a launch has fewer than 2^32 threads
   const int64_t pieces = ((int64_t)c->block_size * (c->head_dim / KVX_FP4_GROUP) * 2 * c->num_kv_heads + 127) / 128;
-  if (total_blocks > (1 << 27) / pieces) return KVX_ERR_INVALID_ARGUMENT;
+  if (total_blocks > ((1 << 27) - 8) / pieces) return KVX_ERR_INVALID_ARGUMENT;
   return st;
 }
 

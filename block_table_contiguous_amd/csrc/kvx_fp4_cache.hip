@@ -245,6 +245,15 @@ struct Runs {
   }
 };
 
+// Runs that leave the buffer, which no block of it finds: one a thread, of the first layer's workgroups (no more runs than blocks
+// count, and a workgroup takes the pieces of 8 blocks at most).
+__device__ __forceinline__ void check_runs(const Fp4CopyArgs& a) {
+  const int64_t i = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x;
+  if (i >= a.total_blocks || i >= constant(a.xfer_count)) return;
+  const int64_t at = a.xfers[i].buf_block;
+  if (at < 0 || at > a.total_blocks || a.xfers[i].num_blocks > a.total_blocks - at) raise(a.err, KVX_DEVERR_BLOCK_RANGE);
+}
+
 // The 4x4 words of four neighbouring lanes transposed: lane c ends with the c-th word of each.
 __device__ __forceinline__ u32x4 transposed(u32x4 v, int c) {
   auto swap = [](uint32_t& low, uint32_t& high, bool upper, auto dpp) {
@@ -345,6 +354,7 @@ __global__ __launch_bounds__(kCopyThreads) void copy_fp4_kernel(Fp4CopyArgs a, G
       }
     }
   };
+  if (blockIdx.y == 0) check_runs(a);
   const uint32_t share = blockIdx.x * (kCopyThreads / 64) + uniform((int32_t)(threadIdx.x / 64));
   for (int l = blockIdx.y; l < a.num_layers; l += gridDim.y) {
     if (share >= (pieces + kPieces - 1) / kPieces) break;

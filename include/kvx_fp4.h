@@ -105,7 +105,7 @@ int64_t kvx_paged_attention_fp4_workspace(const kvx_fp4_cache* cache, const kvx_
 
 /*
  * kvx_pack_fp4 — kvx_pack that quantises: the listed blocks of all layers' 16-bit caches into
- * 4-bit blocks, a third of the bytes to send. Block xfer.src_block + (p - xfer.buf_block) of layer l
+ * 4-bit blocks, 0.27 of the bytes to send. Block xfer.src_block + (p - xfer.buf_block) of layer l
  * becomes block l*total_blocks + p of `buffer`, for every run xfer and its positions p.
  *   cache        sizes, strides and type of each layer's cache; base is not used.
  *   layer_bases  DEVICE array [num_layers] of the layers' caches.

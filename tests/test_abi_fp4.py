@@ -145,6 +145,15 @@ def unpack(c=None, f=None, bases=P, L=2, runs=P, count=P, N=50):
 
 
 @pytest.mark.parametrize("fn", [pack, unpack])
+def test_most_blocks_of_a_launch(fn):
+    """Blocks of one piece of 128 groups: 2^27 - 8 are taken (the odd base is looked at behind the sizes), one more is not."""
+    c = wide(num_kv_heads=1, num_blocks=1, block_stride_bytes=8192)
+    f = fp4(num_kv_heads=1, num_blocks=1 << 27, block_stride_bytes=2 * 1088, base=P + 8)
+    assert fn(c=c, f=f, L=1, N=(1 << 27) - 8) == MISALIGNED
+    assert fn(c=c, f=f, L=1, N=(1 << 27) - 7) == INVALID and fn(c=c, f=f, L=1, N=1 << 27) == INVALID
+
+
+@pytest.mark.parametrize("fn", [pack, unpack])
 def test_transfer_refusals(fn):
     for kw in BAD_CACHES:
         assert fn(f=fp4(**kw)) == INVALID, kw

@@ -246,6 +246,41 @@ def test_transfer_runs(layers, counts):
     run_transfer(seed=4, layers=layers, counts=counts, heads=1, block=8, mode="direct")
 
 
+def test_transfer_runs_that_leave_the_buffer():
+    """The parts of runs inside the buffer move, the others raise the error and touch nothing; of more runs than blocks the
+    first count."""
+    K = kvx()
+    N, nb, block, dim = 6, 9, 16, 64
+    src = torch.randn(nb, block, 2, 2, dim, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).to(DEV)
+    rows = src.cpu().double().numpy().transpose(0, 3, 2, 1, 4)
+    planes = F.to_planes(*F.quantise(rows, F.MOST[torch.bfloat16]))
+    ids = {"inside": ([(2, 0, 2), (7, 2, 4)], [2, 3, 7, 8, None, None], 1),  # ids 9 and 10 are past the cache
+           "behind": ([(2, 0, 2), (0, 2, 2), (4, 4, 5)], [2, 3, 0, 1, 4, 5], 1), "before": ([(3, -1, 3), (0, 2, 4)], [4, 5, 0, 1, 2, 3], 1),
+           "far": ([(1, 0, 2), (0, 1 << 40, 4)], [1, 2] + [None] * 4, 1), "exact": ([(1, 0, 2), (3, 2, 4)], [1, 2, 3, 4, 5, 6], 0)}
+    for name, (runs, want, bad) in ids.items():
+        log(name)
+        table = torch.zeros(N, 4, dtype=torch.int64)
+        for i, (b, at, n) in enumerate(runs):
+            table[i] = torch.tensor([b, b, at, n])  # the request in the last field's upper half is 0
+        xfers, count = table.to(DEV), torch.tensor([len(runs)], dtype=torch.int64, device=DEV)
+        buf = torch.full(F.shape_of(N + 1, 2, F.plane_bytes(block, dim), F.LAYOUTS4[0]), 0xcd, dtype=torch.uint8, device=DEV)
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        K.kvx_pack_fp4(K.layer_base_table([src]), src, xfers, count, N, buf, err_flag=err)
+        assert int(err.item()) == (K.DEVERR_BLOCK_RANGE if bad else 0), name
+        got = buf.cpu().numpy()
+        for p, b in enumerate(want):
+            assert np.array_equal(got[p], np.full_like(got[p], 0xcd) if b is None else planes[b]), (name, p)
+        assert (got[N] == 0xcd).all()
+        dst = torch.full_like(src, 7.0)
+        err.zero_()
+        K.kvx_unpack_fp4(buf, K.layer_base_table([dst]), dst, xfers, count, N, err_flag=err)
+        assert int(err.item()) == (K.DEVERR_BLOCK_RANGE if bad else 0), name
+        held = {b for b in want if b is not None}
+        for b in range(nb):
+            v = torch.from_numpy(F.values(*F.from_planes(planes[b], block, dim))).permute(2, 1, 0, 3).to(src.dtype)
+            assert torch.equal(dst[b].cpu(), v if b in held else torch.full_like(v, 7.0)), (name, b)
+
+
 def test_transfer_bad_ids():
     run_transfer(seed=5, counts=(3, 5), bad=True)
 
