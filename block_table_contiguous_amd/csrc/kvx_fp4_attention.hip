@@ -460,9 +460,8 @@ __device__ __forceinline__ f32x16 product(Fp16, u32x4 a, u32x4 b, f32x16 c) {
 
 // Many rows: 128 of them a workgroup, 32 a wavefront, and 64 slots a step, which the four wavefronts widen to 16 bits on their
 // way to LDS, 16 slots each. Scores transposed as above, with the 32x32x16 products.
-//   BY_BLOCK: 16 slots always lie in one block, whose address is formed once a wavefront, in scalar registers.
 //   SHARED: the grid's workgroups take equal shares of the whole batch's steps (see Shares).
-template <class E, int DP, bool BY_BLOCK, bool SHARED>
+template <class E, int DP, bool SHARED>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_rows_kernel(AttendArgs args, BlockDiv div, Split sp) {
   const AttendArgs a = argument<AttendArgs>();
   constexpr int ROWS = 128, BN = 64, KW = 16, KT = 2, KSTEPS = DP / 16, DT = DP / 32;
@@ -523,7 +522,6 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_rows_kernel
     x = find_rows<ROWS>(a, sp.tiles - 1 - (round & 1 ? back - 1 - (index - round * per) : index), group, cap, lane);
     if (x.tile < 0 || (int64_t)x.tile * ROWS >= (int64_t)x.tokens * group) return;
   }
-  int errs = 0;
   bool bad_blocks = false;
   for (;;) {
   const AttendArgs a = argument<AttendArgs>();
@@ -581,7 +579,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_rows_kernel
   const float c1 = a.scale * kLog2e;
 
   auto load_id = [&](int t) -> int32_t {
-    const int b = block_of(div, t * BN + w * KW + (BY_BLOCK ? 0 : slot));
+    const int b = block_of(div, t * BN + w * KW + slot);
     return gload<int32_t>(table + (b < cols ? b : cols - 1));
   };
   u32x4 rk[KS], rv[KS];
@@ -589,33 +587,14 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_rows_kernel
   uint32_t ok_mask = 0;
   auto fetch = [&](int t, int32_t id) {
     // a slot that is not there is read from the cache's first rows; its scale of V becomes 0, and its weight is
-    const int j = t * BN + w * KW + (BY_BLOCK ? 0 : slot);
-    const char *e, *s;
-    if constexpr (BY_BLOCK) {
-      const int32_t block = uniform(id);
-      int there = kend - j < 16 ? kend - j : 16;
-      if (there < 0) there = 0;
-      ok_mask = 0;
-      const char* k = base;
-      int o = 0;
-      if ((uint32_t)block < (uint64_t)a.cache.num_blocks) {
-        k += block * a.cache.block_stride_bytes;
-        o = j - block_of(div, j) * div.size;
-        ok_mask = (1u << there) - 1;
-      } else if (there > 0) {
-        bad_blocks = true;
-      }
-      e = k + (int64_t)o * (dim / 2) + slot * (dim / 2);
-      s = k + scales + (int64_t)o * groups + slot * groups;
-    } else {
-      const bool in = j < kend, ok = in && (uint32_t)id < (uint64_t)a.cache.num_blocks;
-      if (in && !ok) errs |= KVX_DEVERR_BLOCK_RANGE;
-      ok_mask = (uint32_t)(__ballot(ok) & 0xffff);
-      const int64_t o = ok ? j - block_of(div, j) * div.size : 0;
-      const char* k = base + (ok ? id * a.cache.block_stride_bytes : 0);
-      e = k + o * (dim / 2);
-      s = k + scales + o * groups;
-    }
+    const int j = t * BN + w * KW + slot;
+    const bool wanted = j < kend, ok = wanted && (uint32_t)id < (uint64_t)a.cache.num_blocks;
+    bad_blocks |= wanted && !ok;
+    ok_mask = (uint32_t)(__ballot(ok) & 0xffff);
+    const int64_t o = ok ? j - block_of(div, j) * div.size : 0;
+    const char* k = base + (ok ? id * a.cache.block_stride_bytes : 0);
+    const char* e = k + o * (dim / 2);
+    const char* s = k + scales + o * groups;
 #pragma unroll
     for (int c = 0; c < KS; ++c) {
       const int at = c * 4 + quarter;
@@ -852,20 +831,17 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_fp4_rows_kernel
     } while (tiles == 0);
   }
   }
-  if (bad_blocks) errs |= KVX_DEVERR_BLOCK_RANGE;
-  if (errs) raise(a.err, errs);
+  if (bad_blocks) raise(a.err, KVX_DEVERR_BLOCK_RANGE);
 }
 
 template <class E, int DP>
 void launch_attend(const AttendArgs& a, BlockDiv div, const Split& sp, int rows, hipStream_t stream) {
   const int heads = a.cache.num_kv_heads;
-  const bool by_block = a.cache.block_size % 16 == 0;
   if (sp.shares == 0) {
     const dim3 grid((unsigned)(sp.tiles * heads));
     if (rows == 16) attend_fp4_kernel<E, DP, 1, false><<<grid, 256, 0, stream>>>(a, div, sp);
     else if (rows == 32) attend_fp4_kernel<E, DP, 2, false><<<grid, 256, 0, stream>>>(a, div, sp);
-    else if (by_block) attend_fp4_rows_kernel<E, DP, true, false><<<grid, 256, 0, stream>>>(a, div, sp);
-    else attend_fp4_rows_kernel<E, DP, false, false><<<grid, 256, 0, stream>>>(a, div, sp);
+    else attend_fp4_rows_kernel<E, DP, false><<<grid, 256, 0, stream>>>(a, div, sp);
     return;
   }
   const dim3 grid((unsigned)(sp.shares * heads));
@@ -884,8 +860,7 @@ void launch_attend(const AttendArgs& a, BlockDiv div, const Split& sp, int rows,
     attend_fp4_kernel<E, DP, 2, true><<<grid, 256, 0, stream>>>(a, div, sp);
     join_kernel<E, 32, 128, kFp4Extra><<<join, 256, 0, stream>>>(a, sp);
   } else {
-    if (by_block) attend_fp4_rows_kernel<E, DP, true, true><<<grid, 256, 0, stream>>>(a, div, sp);
-    else attend_fp4_rows_kernel<E, DP, false, true><<<grid, 256, 0, stream>>>(a, div, sp);
+    attend_fp4_rows_kernel<E, DP, true><<<grid, 256, 0, stream>>>(a, div, sp);
     join_kernel<E, 128, 64><<<join, 256, 0, stream>>>(a, sp);
   }
 }
@@ -900,7 +875,7 @@ void launch_dims(const AttendArgs& a, BlockDiv div, const Split& sp, int rows, h
 }  // namespace
 
 hipError_t launch_attention_fp4(const AttendArgs& a, hipStream_t stream) {
-  const Fp4Plan p = plan_attention_fp4(a.cache, a.batch, a.num_heads);
+  const Fp4Plan p = plan_attention_fp4(a.cache, a.batch, a.num_heads, a.window);
   Split sp = {fp4_shares_within(p, a.cache, a.workspace_bytes), p.tiles, nullptr, nullptr};
   if (sp.shares > 0) {
     sp.acc = (float*)a.workspace;  // first: rows of 16-byte vectors

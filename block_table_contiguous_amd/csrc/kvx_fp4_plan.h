@@ -8,10 +8,14 @@
 namespace kvx {
 
 // A request's rows of one KV head are taken 16 or 32 at a time, by four wavefronts that take 32 slots each of every 128, or, where there
-// are more, 128 at a time, 64 slots a step. Where the tiles do not fill the GPU, or a decode batch's contexts are uneven, the
-// batch's steps are shared out evenly (see Shares) to as many workgroups as the GPU holds, of 256 slots at least (with 512, one request of 8000 slots takes 18.1 us
-// and not 16.1).
-constexpr int kFp4Extra = 2;  // steps of 128 slots that the start of a tile of few rows counts for
+// are more, 128 at a time, 64 slots a step, which reads a context once for up to 128 rows but widens it slower than 16-row tiles stream
+// it. 32 requests of up to 8192 slots, 32 heads on 8, dimension 128: 1 token (4 rows) takes 44 us in tiles of 16 and 58 in tiles of 32;
+// 8 tokens 68 in tiles of 32 and 107 in tiles of 128; 16 tokens, two tiles of 32, 93 and 112; 24 tokens 122 and 110. At
+// dimension 256, where a CU holds one tile of 128, 24 tokens 312 and 329 (439 unshared), 32 tokens 377 and 334.
+//
+// Where the tiles do not fill the GPU, or are uneven, the batch's steps are shared out evenly (see Shares) to as many workgroups as the
+// GPU holds, of 256 slots at least (with 512, one request of 8000 slots takes 18.1 us and not 16.1).
+constexpr int kFp4Extra = 2;  // steps that the start of a tile of few rows counts for: the decode batch takes 38.3 us, with 0 40.4
 constexpr int64_t kFp4MaxWorkgroups = (1 << 24) - 1;  // of 256 threads: a launch has fewer than 2^32
 
 struct Fp4Plan {
@@ -19,11 +23,12 @@ struct Fp4Plan {
   int32_t tiles, shares;
   int64_t busy;  // tiles that have rows, by the hints
 };
-inline Fp4Plan plan_attention_fp4(const kvx_paged_cache& c, const kvx_batch& b, int32_t num_heads) {
+inline Fp4Plan plan_attention_fp4(const kvx_paged_cache& c, const kvx_batch& b, int32_t num_heads, int64_t window = INT64_MAX) {
   const int64_t group = num_heads / c.num_kv_heads;
   const int64_t longest = b.max_query_len < b.num_tokens ? b.max_query_len : b.num_tokens;
+  const int dim = c.head_dim;
   Fp4Plan p;
-  p.rows = longest * group <= 16 ? 16 : longest * group <= 32 ? 32 : 128;
+  p.rows = longest * group <= 16 ? 16 : longest * group <= (dim > 128 ? 96 : 64) ? 32 : 128;
   // tiles of few rows also have to be few enough for a launch, as those of requests that keep to the hint are
   if ((b.num_tokens * group / p.rows + b.num_reqs) * c.num_kv_heads > kFp4MaxWorkgroups) p.rows = 128;
   const bool few = p.rows < 128;
@@ -36,13 +41,22 @@ inline Fp4Plan plan_attention_fp4(const kvx_paged_cache& c, const kvx_batch& b, 
   // The workgroups that the registers leave room for, 1 to 4 a CU. 32 requests of up to 8192 slots, 32 heads on 8: one token of
   // dimension 256 takes 82 us, with 768 158; 8 tokens of 128 66 us, with 768 84; one of 128 38 us, with 512 46 and with 1024 49; one of
   // 64 34 us, with 768 36.
-  const int dim = c.head_dim;
-  const int fill = p.rows == 16 ? (dim > 128 ? 512 : dim > 64 ? 768 : 1024) : dim > 128 ? 256 : few && dim <= 64 ? 768 : 512;
-  int64_t shares = fill / c.num_kv_heads, most = busy * (context / 256);
+  const int64_t fill = p.rows == 16 ? (dim > 128 ? 512 : dim > 64 ? 768 : 1024) : dim > 128 ? 256 : few && dim <= 64 ? 768 : 512;
+  int64_t shares = fill / c.num_kv_heads, most = busy * (context / 256), least = few ? busy / 4 : busy;
   if (shares > most) shares = most;
-  const bool uneven = busy * c.num_kv_heads < (few ? 4 * fill : fill);
+  // Tiles of 128 rows that fill the GPU, up to four times: shares take every tile of a request to be as long as its context, so only
+  // where they nearly are (no prompts, no window), and the rounds come out uneven: by requests, or by a last round that is
+  // part empty. 2304 tokens over 32768 slots, 32 heads on 8, take 1240 us and not 1693; 4096, two full rounds, 2029 and not 2004; 32 chunks of
+  // up to 517 over up to 9216, 8 heads on one, 300 and not 397; a prompt of 8192 tokens 278 and not 195.
+  const int64_t work = busy * c.num_kv_heads;
+  bool uneven = work < (few ? 4 * fill : fill);
+  if (!few && !uneven && work < 4 * fill && longest <= context / 4 && window >= context &&
+      (b.num_reqs > 1 || 8 * work < 7 * ((work + fill - 1) / fill * fill))) {
+    uneven = true;
+    least = busy / 4;
+  }
   p.busy = busy;
-  p.shares = uneven && shares > (few ? busy / 4 : busy) ? (int32_t)shares : 0;
+  p.shares = uneven && shares > least ? (int32_t)shares : 0;
   return p;
 }
 

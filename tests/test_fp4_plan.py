@@ -27,7 +27,7 @@ def plans(tmp_path_factory):
     return run
 
 
-BATCHES = [(1, 1, 1, 131072, 32, 8, 128), (16, 16, 1, 8192, 32, 8, 128), (32, 32, 1, 8192, 32, 8, 128),
+BATCHES = [(1, 1, 1, 131072, 32, 8, 128), (1, 2304, 2304, 32768, 32, 8, 128), (32, 9000, 517, 9216, 8, 1, 128), (16, 16, 1, 8192, 32, 8, 128), (32, 32, 1, 8192, 32, 8, 128),
            (72, 72, 1, 8192, 32, 8, 64), (300, 300, 1, 4096, 8, 1, 128), (8, 4000, 517, 9216, 8, 1, 128),
            (1, 100, 100, 60000, 4, 1, 256), (3, 12, 4, 9000, 8, 2, 64), (5, 20, 4, 9000, 56, 8, 256)]
 
@@ -48,10 +48,18 @@ def test_a_small_workspace_is_no_worse_than_none(plans, batch):
     assert plans([(*batch, 0)])[0]["shares"] == 0
 
 
-@pytest.mark.parametrize("tokens,heads,kv,rows", [(1, 16, 1, 16), (1, 17, 1, 32), (2, 16, 1, 32), (4, 8, 1, 32), (3, 11, 1, 128),
-                                                  (1, 128, 8, 16), (517, 8, 1, 128)])
-def test_rows_of_a_tile(plans, tokens, heads, kv, rows):
-    assert plans([(2, 2 * tokens, tokens, 5000, heads, kv, 128, -1)])[0]["rows"] == rows
+@pytest.mark.parametrize("tokens,heads,kv,rows,wide", [(1, 16, 1, 16, 16), (1, 17, 1, 32, 32), (2, 16, 1, 32, 32), (8, 8, 1, 32, 32),
+                                                       (5, 13, 1, 128, 32), (12, 8, 1, 128, 32), (97, 1, 1, 128, 128),
+                                                       (1, 128, 8, 16, 16), (517, 8, 1, 128, 128)])
+def test_rows_of_a_tile(plans, tokens, heads, kv, rows, wide):
+    for dim, want in ((128, rows), (256, wide)):
+        assert plans([(2, 2 * tokens, tokens, 5000, heads, kv, dim, -1)])[0]["rows"] == want
+
+
+@pytest.mark.parametrize("reqs,query,context,shared", [(1, 2048, 32768, 0), (1, 2304, 32768, 64), (1, 4096, 32768, 0), (1, 2560, 32768, 64),
+                                                       (3, 2048, 32768, 64), (1, 2304, 9000, 0), (4, 4096, 32768, 0)])
+def test_shares_of_tiles_that_fill_the_gpu(plans, reqs, query, context, shared):
+    assert plans([(reqs, reqs * query, query, context, 32, 8, 128, -1)])[0]["planned"] == shared
 
 
 def test_the_grid_stays_within_what_a_launch_can_have(plans):

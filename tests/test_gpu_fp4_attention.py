@@ -84,6 +84,28 @@ def test_split_contexts(lens, split, dtype):
     run(F.Case4(7, lens, heads=8, kv_heads=1, dim=128, dtype=dtype), split=split)
 
 
+@pytest.mark.parametrize("split", [True, False])
+@pytest.mark.parametrize("lens", [[(9, 100), (16, 2700), (1, 5), (0, 3), (12, 12)], [(11, 40), (13, 1300)]])
+def test_several_tiles_of_few_rows(lens, split):
+    """33 to 64 rows a request: two tiles of 32."""
+    run(F.Case4(21, lens, heads=8, kv_heads=2, dim=128), split=split)
+    run(F.Case4(21, lens, heads=8, kv_heads=2, dim=64, dtype="fp16"), split=split, window=30)
+
+
+@pytest.mark.parametrize("split", [True, False])
+def test_three_tiles_of_few_rows(split):
+    run(F.Case4(22, [(24, 500), (3, 1900), (17, 30)], heads=4, kv_heads=1, dim=256), split=split)
+
+
+@pytest.mark.parametrize("window,causal", [(0, True), (0, False), (200, True)])
+def test_shares_of_tiles_that_fill_the_gpu(window, causal):
+    """640 and 768 tiles of 128 rows, shared out to 512 workgroups (with the window: not)."""
+    run(F.Case4(23, [(129, 700), (129, 130), (140, 600), (5, 700), (0, 9), (129, 333)], heads=64, kv_heads=64, dim=64, dtype="fp16"),
+        window=window, causal=causal)
+    if not window:
+        run(F.Case4(24, [(1100, 5000)], heads=64, kv_heads=64, dim=32), causal=causal, scale=0.3)
+
+
 def test_many_requests():
     rng = np.random.default_rng(8)
     lens = [(int(rng.integers(0, 4)), int(rng.integers(0, 90))) for _ in range(150)]
