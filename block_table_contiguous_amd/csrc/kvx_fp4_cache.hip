@@ -12,8 +12,8 @@ namespace {
 // the write of rotated new rows
 // --------------------------------------------------------------------------------------
 
-// Data that is read, or written, once goes past the caches (9461 tokens of 32 + 8 heads rotated and written: 57 us with the caches'
-// default policy for the loads, 48 so).
+// Data that is read, or written, once goes past the caches: with cached loads packing 48 layers takes 414 us and not 400, with cached
+// stores both directions 937 us and not 905 (of an earlier step).
 template <class T>
 __device__ __forceinline__ T gload_once(const void* p) {
   return __builtin_nontemporal_load((const __attribute__((address_space(1))) T*)p);
@@ -36,7 +36,8 @@ __device__ __forceinline__ float sticky(double x) {
 // key is rounded to 4 bits, and 32 bits on the way there would decide some of the elements next to a border between two codes.
 // Rows are moved as 16-byte vectors, the first on their way while the angles are formed and the next while a thread turns its own: of K
 // and V four neighbouring lanes hold a group of 32 elements, eight each, with the partners of the eight beside them; of q a thread holds
-// whole pairs. Bound by HBM bytes for many tokens, by a launch and the chain positions, angles, stores for a few.
+// whole pairs. Bound by HBM bytes for many tokens (9461 tokens of 32 + 8 heads, 243 MB: 45 us, 5.4 TB/s; with 128, 384 and 512 threads a token 53, 62
+// and 61 us), by a launch and the chain positions, angles, stores for a few (32 tokens: 5 us). Angles in 32 bits for K save nothing.
 struct RopeUnits {
   Divisor of_head, of_q_head;  // vectors of a K or V head, units of a q head
   int32_t kv, all;             // vectors of K and V, and all units
@@ -277,9 +278,11 @@ __device__ __forceinline__ uint32_t of_lane(uint32_t x) {  // of the four neighb
 
 // A wavefront takes 128 groups at a time, 8 KiB of the 16-bit side, and kPieces such pieces one after another, the next one's loads
 // before the present one's stores. On the 16-bit side four lanes hold a group, 16 bytes each; on the 4-bit side a lane holds one, and words
-// change lanes between the two, so that both move 1 KiB an instruction. Bound by HBM bytes, read and written once.
+// change lanes between the two, so that both move 1 KiB an instruction. Bound by HBM bytes, read and written once: 48 layers of
+// 4608 blocks of 8 KiB (2.29 GB on both sides) are packed in 400 us, 5.7 TB/s, and unpacked to random blocks in 429 us, 5.3 TB/s; with 1, 4
+// and 8 pieces a wavefront the two took 915, 887 and 916 us together where 2 took 842, with the groups in the 16-bit side's order 907.
 //   EVEN, where rows are 1, 2, 4 or 8 groups and planes whole times 16: 16 groups are rows of one plane, whose place the scalar
-//   unit finds; a lane's place among them never changes.
+//   unit finds; a lane's place among them never changes. Packing so takes 400 us and not 420; unpacking is no faster.
 constexpr int kPiece = 128, kLoads = kPiece / 16, kPieces = 2;
 template <class E, bool PACK, bool EVEN>
 __global__ __launch_bounds__(kCopyThreads) void copy_fp4_kernel(Fp4CopyArgs a, Groups g, uint32_t pieces) {
@@ -380,9 +383,13 @@ __global__ __launch_bounds__(kCopyThreads) void copy_fp4_kernel(Fp4CopyArgs a, G
 
 template <class E, bool PACK>
 void launch_copy_type(const Fp4CopyArgs& a, const Groups& g, uint32_t pieces, dim3 grid, hipStream_t stream) {
-  if (16 % g.per_row.by == 0 && g.per_plane.by % 16 == 0)
-    copy_fp4_kernel<E, PACK, true><<<grid, kCopyThreads, 0, stream>>>(a, g, pieces);
-  else copy_fp4_kernel<E, PACK, false><<<grid, kCopyThreads, 0, stream>>>(a, g, pieces);
+  if constexpr (PACK) {
+    if (16 % g.per_row.by == 0 && g.per_plane.by % 16 == 0) {
+      copy_fp4_kernel<E, true, true><<<grid, kCopyThreads, 0, stream>>>(a, g, pieces);
+      return;
+    }
+  }
+  copy_fp4_kernel<E, PACK, false><<<grid, kCopyThreads, 0, stream>>>(a, g, pieces);
 }
 
 template <bool PACK>
