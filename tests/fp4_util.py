@@ -143,6 +143,8 @@ def attend(case: Case4, dev, causal=True, window=0, scale=None, split=True, out=
     lse = torch.full(q.shape[:2], 7.0, device=q.device)
     err = torch.zeros(1, dtype=torch.int32, device=q.device)
     n, c = max([n for n, _ in case.lens] + [0]), max(list(case.context) + [0])
+    if split:
+        c = max(int(c), 2000)  # a hint may be high: short contexts are shared out as well
     ws = workspace
     if ws is None and split:
         ws = K.new_attention_workspace_fp4(q, cache, len(case.lens), n, max(int(c), 0), layout=case.layout)

@@ -62,6 +62,11 @@ def test_shares_of_tiles_that_fill_the_gpu(plans, reqs, query, context, shared):
     assert plans([(reqs, reqs * query, query, context, 32, 8, 128, -1)])[0]["planned"] == shared
 
 
+@pytest.mark.parametrize("context,shares", [(512, 0), (896, 0), (897, 96), (4096, 96)])
+def test_few_slots_are_not_shared_out(plans, context, shares):
+    assert plans([(40, 40, 1, context, 32, 8, 128, -1)])[0]["planned"] == shares
+
+
 def test_the_grid_stays_within_what_a_launch_can_have(plans):
     """A tile is a workgroup of 256 threads for every KV head, and a launch has fewer than 2^32 threads, however long the
     requests are that the hint calls short."""

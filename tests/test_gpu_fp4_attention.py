@@ -92,6 +92,13 @@ def test_several_tiles_of_few_rows(lens, split):
     run(F.Case4(21, lens, heads=8, kv_heads=2, dim=64, dtype="fp16"), split=split, window=30)
 
 
+@pytest.mark.parametrize("window", [900, 1000, 1500, 2300])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens", [[(1, 2700), (3, 1500), (2, 950)], [(1, 2700), (70, 2000), (20, 20), (2, 950)]])
+def test_windows_in_split_contexts(lens, causal, window):
+    run(F.Case4(25, lens, heads=4, kv_heads=2, dim=64), causal=causal, window=window)
+
+
 @pytest.mark.parametrize("split", [True, False])
 def test_three_tiles_of_few_rows(split):
     run(F.Case4(22, [(24, 500), (3, 1900), (17, 30)], heads=4, kv_heads=1, dim=256), split=split)
@@ -128,7 +135,7 @@ def test_wrong_hints_change_nothing(lens):
         A.check("lse", lse, want_lse, tol_lse)
 
 
-@pytest.mark.parametrize("lens", [[(1, 2000), (1, 900)], [(64, 700)]])
+@pytest.mark.parametrize("lens", [[(1, 2000), (1, 900)], [(64, 1700)]])
 def test_small_workspaces_and_repeats(lens):
     """A workspace of any size, down to none; the same call gives the same bits."""
     case = F.Case4(10, lens, heads=8, kv_heads=1)
