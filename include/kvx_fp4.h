@@ -63,7 +63,8 @@ int64_t kvx_fp4_plane_bytes(int32_t block_size, int32_t head_dim);
  * kvx_rope_and_cache_fp4 — kvx_rope_and_cache for a 4-bit cache: rotate the new tokens' queries
  * and keys by their positions, and write the rotated K row and the V row of each token into its slot,
  * quantised on the way. Arguments, positions, padding and errors as kvx_rope_and_cache. A rotated key is
- * formed in 64 bits and rounded once, to its 4-bit value; a rotated query as there.
+ * formed in 64 bits and rounded once, to its 4-bit value (beyond the range of 32 bits it counts as infinite); a rotated
+ * query as there.
  *   key_out, value_out  [num_tokens][num_kv_heads][head_dim] at the given strides, both or neither NULL: what
  *              the cache holds of each token, in the 16-bit type, for an attention over the new
  *              rows that sees them as later steps will. Written for tokens without a slot as
