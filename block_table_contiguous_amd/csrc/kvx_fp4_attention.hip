@@ -853,6 +853,7 @@ void launch_attend(const AttendArgs& a, BlockDiv div, const Split& sp, int rows,
   }
   const dim3 grid((unsigned)(sp.shares * heads));
   // a tile's rows are joined by one workgroup, or by several while that is up to 2048 in all and they have 32 threads' work each
+  // (177 tiles of 128 rows: 13.4 us by 11 workgroups each, 14.3 by 4, 19.8 by 2, 14.7 by 16)
   const int64_t blocks = (int64_t)sp.tiles * heads;
   const int64_t longest = a.batch.max_query_len < a.batch.num_tokens ? a.batch.max_query_len : a.batch.num_tokens;
   const int64_t most = longest * (a.num_heads / heads) * a.cache.head_dim / 128;
