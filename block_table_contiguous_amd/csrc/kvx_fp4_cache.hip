@@ -25,11 +25,14 @@ __device__ __forceinline__ void gstore_once(void* p, T v) {
 
 constexpr int kRopeThreads = 256;
 
-// A 64-bit number to 32 bits so that a later rounding to fewer bits is as if it were the only one: toward zero, with the
-// last bit set where anything was cut off (no value that the 4-bit rounding or the scale's bound breaks at has it set).
+// A 64-bit number to 32 bits so that a later rounding to 4 bits is as if it were the only one: its upper half, with the last bit set
+// where anything was cut off. No value that the 4-bit rounding or the scale's bound breaks at has that bit set. The half has 21
+// bits, so the cast is exact down to 2^-129, the smallest border of any scale, although 32 bits end at 2^-149; what lies below ends
+// there at most, on a tie that goes to 0, which is what it is itself.
 __device__ __forceinline__ float sticky(double x) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, x), low = b & 0x1fffffffull;
-  return (float)__builtin_bit_cast(double, (b ^ low) | (low ? 0x20000000ull : 0));
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t upper = (uint32_t)(b >> 32) | (uint32_t)((uint32_t)b != 0);
+  return (float)__builtin_bit_cast(double, (uint64_t)upper << 32);
 }
 
 // One workgroup a token. Its first rot_dim/2 threads form the angles' cosines and sines, once for all heads and in 64 bits: a rotated
