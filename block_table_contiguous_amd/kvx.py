@@ -930,7 +930,9 @@ def new_fp4_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim:
     describes it:
       blocks_heads_kv  [blocks][heads][K,V][plane]
       blocks_kv_heads  [blocks][K,V][heads][plane]
-      kv_blocks_heads  [K,V][blocks][heads][plane]"""
+      kv_blocks_heads  [K,V][blocks][heads][plane]
+    The tensor remembers block_size and head_dim, which its shape does not tell (16 slots of 128
+    elements are as many bytes as 32 of 64); its views and copies do not."""
     import torch
 
     if layout not in _FP4_AXES:
@@ -938,14 +940,21 @@ def new_fp4_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim:
     shape = [0, 0, 0, fp4_plane_bytes(block_size, head_dim)]
     for axis, n in zip(_FP4_AXES[layout], (num_blocks, num_kv_heads, 2)):
         shape[axis] = int(n)
-    return torch.zeros(shape, dtype=torch.uint8, device=device)
+    cache = torch.zeros(shape, dtype=torch.uint8, device=device)
+    cache._kvx_rows = (int(block_size), int(head_dim))
+    return cache
 
 
-def fp4_cache(kv_cache, head_dim: int, dtype, layout: str = "blocks_heads_kv") -> Fp4Cache:
+def fp4_cache(kv_cache, head_dim: int, dtype, layout: str = "blocks_heads_kv",
+              block_size: Optional[int] = None) -> Fp4Cache:
     """A 4-D uint8 tensor of new_fp4_cache's layouts (any strides whose planes are dense) as the
     struct that the calls below take, for rows of head_dim elements and calls whose other rows are
     of dtype. They make it from the tensor themselves; a caller that makes the same call many times
-    can make it once and pass it instead."""
+    can make it once and pass it instead.
+    The planes have to be fp4_plane_bytes(block_size, head_dim) long. Without block_size a tensor
+    from new_fp4_cache is taken as it was made, and refused for other rows. Of any other tensor
+    (a view or a copy among them) the block size is what the planes hold of such rows: state it
+    there, or rows of a wrong head_dim find a block size that fits them."""
     shape, stride, axes = kv_cache.shape, kv_cache.stride(), _FP4_AXES.get(layout)
     if axes is None:
         raise ValueError(f"unknown layout {layout}")
@@ -955,9 +964,15 @@ def fp4_cache(kv_cache, head_dim: int, dtype, layout: str = "blocks_heads_kv") -
     if stride[3] != 1:
         raise ValueError("kvx: the planes of a 4-bit cache must be dense")
     blocks, heads, plane = shape[b], shape[h], shape[3]
-    # a plane grows by more than its padding with every token, so its size says how many there are
-    tokens = plane * FP4_GROUP // (17 * head_dim) if head_dim > 0 else 0
-    if tokens < 1 or head_dim % FP4_GROUP or (tokens * 17 * head_dim // FP4_GROUP + 15) // 16 * 16 != plane:
+    if block_size is not None:
+        tokens = int(block_size)
+    elif (made := getattr(kv_cache, "_kvx_rows", None)) is not None:
+        tokens, dim = made
+        if dim != head_dim:
+            raise ValueError(f"kvx: this 4-bit cache was made for rows of {dim} elements")
+    else:  # a plane grows by more than its padding with every token, so its size says how many there are
+        tokens = plane * FP4_GROUP // (17 * head_dim) if head_dim > 0 else 0
+    if tokens < 1 or head_dim < 1 or head_dim % FP4_GROUP or (tokens * 17 * head_dim // FP4_GROUP + 15) // 16 * 16 != plane:
         raise ValueError("kvx: the last dimension of a 4-bit cache must be fp4_plane_bytes(block_size, head_dim)")
     # the stride of a dimension with one entry is never used and may be anything
     c = Fp4Cache(kv_cache.data_ptr(), blocks, stride[b] if blocks > 1 else 0, stride[w], stride[h] if heads > 1 else 0, tokens,
@@ -966,23 +981,25 @@ def fp4_cache(kv_cache, head_dim: int, dtype, layout: str = "blocks_heads_kv") -
     return c
 
 
-def _fp4(kv_cache, rows, layout) -> Fp4Cache:
+def _fp4(kv_cache, rows, layout, block_size) -> Fp4Cache:
     """kv_cache for a call whose rows are [tokens][heads][head_dim] like `rows`."""
     if type(kv_cache) is Fp4Cache:
+        if block_size is not None and block_size != kv_cache.block_size:
+            raise ValueError("kvx: the struct of the 4-bit cache has another block_size")
         return kv_cache
     if rows.dim() != 3:
         raise ValueError("kvx: rows must be [num_tokens][heads][head_dim]")
-    return fp4_cache(kv_cache, rows.shape[2], rows.dtype, layout)
+    return fp4_cache(kv_cache, rows.shape[2], rows.dtype, layout, block_size)
 
 
 def kvx_rope_and_cache_fp4(query, key, value, positions, inv_freq, pair_axis: Sequence[int], slot_mapping, kv_cache,
                            query_out, key_out=None, value_out=None, layout: str = "blocks_heads_kv",
-                           interleaved: bool = False, err_flag=None, stream=None):
+                           interleaved: bool = False, err_flag=None, stream=None, block_size: Optional[int] = None):
     """kvx_rope_and_cache into a 4-bit cache (a tensor of new_fp4_cache's layouts, or fp4_cache of
-    it). key_out and value_out ([num_tokens][num_kv_heads][head_dim], both or neither) get what the
+    it; block_size as there). key_out and value_out ([num_tokens][num_kv_heads][head_dim], both or neither) get what the
     cache then holds of each token; they must not overlap key and value."""
     torch = _th()
-    c = _fp4(kv_cache, key, layout)
+    c = _fp4(kv_cache, key, layout, block_size)
     _want(slot_mapping, torch.int64, "slot_mapping")
     _want(positions, torch.int64, "positions")
     _want(inv_freq, torch.float32, "inv_freq")
@@ -1024,9 +1041,9 @@ def kvx_rope_and_cache_fp4(query, key, value, positions, inv_freq, pair_axis: Se
 
 
 def attention_workspace_fp4_bytes(query, kv_cache, num_reqs: int, max_query_len: int, max_context_len: int,
-                                  layout: str = "blocks_heads_kv") -> int:
+                                  layout: str = "blocks_heads_kv", block_size: Optional[int] = None) -> int:
     """Bytes of workspace with which kvx_paged_attention_fp4 splits such a batch as far as pays."""
-    c = _fp4(kv_cache, query, layout)
+    c = _fp4(kv_cache, query, layout, block_size)
     b = Batch(None, None, None, 0, 0, query.shape[0], int(max_query_len), int(max_context_len), int(num_reqs))
     n = _F["kvx_paged_attention_fp4_workspace"](c, b, query.shape[1])
     if n < 0:
@@ -1035,21 +1052,22 @@ def attention_workspace_fp4_bytes(query, kv_cache, num_reqs: int, max_query_len:
 
 
 def new_attention_workspace_fp4(query, kv_cache, num_reqs: int, max_query_len: int, max_context_len: int,
-                                layout: str = "blocks_heads_kv"):
+                                layout: str = "blocks_heads_kv", block_size: Optional[int] = None):
     """A workspace of attention_workspace_fp4_bytes (one per concurrent stream or captured graph)."""
     import torch
 
-    n = attention_workspace_fp4_bytes(query, kv_cache, num_reqs, max_query_len, max_context_len, layout)
+    n = attention_workspace_fp4_bytes(query, kv_cache, num_reqs, max_query_len, max_context_len, layout, block_size)
     return torch.empty(n, dtype=torch.uint8, device=query.device)
 
 
 def kvx_paged_attention_fp4(query, kv_cache, block_table, q_offsets, context_lens, out, lse=None,
                             scale: Optional[float] = None, causal: bool = True, window: int = 0,
                             max_query_len: Optional[int] = None, max_context_len: Optional[int] = None,
-                            workspace=None, layout: str = "blocks_heads_kv", err_flag=None, stream=None):
+                            workspace=None, layout: str = "blocks_heads_kv", err_flag=None, stream=None,
+                            block_size: Optional[int] = None):
     """kvx_paged_attention over a 4-bit cache (a tensor of new_fp4_cache's layouts, or fp4_cache of
-    it), with a workspace of new_attention_workspace_fp4."""
-    c = _fp4(kv_cache, query, layout)
+    it; block_size as there), with a workspace of new_attention_workspace_fp4."""
+    c = _fp4(kv_cache, query, layout, block_size)
     b, heads, qs = _batch(query, c, block_table, q_offsets, context_lens, max_query_len, max_context_len)
     os_ = _dense_rows(out, b.num_tokens, heads, query.dtype, c, "out")
     if lse is not None:
@@ -1072,7 +1090,7 @@ def _transfer_fp4(layer_bases, kv_cache, xfers, xfer_count, total_blocks: int, b
     torch = _th()
     c = _cache(kv_cache, layout)
     f = buffer if type(buffer) is Fp4Cache else fp4_cache(
-        buffer, c.head_dim, torch.bfloat16 if c.dtype == DTYPE_BF16 else torch.float16, buffer_layout)
+        buffer, c.head_dim, torch.bfloat16 if c.dtype == DTYPE_BF16 else torch.float16, buffer_layout, c.block_size)
     _want(layer_bases, torch.int64, "layer_bases")
     _want_runs(xfers, xfer_count, total_blocks)
     if (f.block_size, f.num_kv_heads, f.head_dim, f.dtype) != (c.block_size, c.num_kv_heads, c.head_dim, c.dtype):
