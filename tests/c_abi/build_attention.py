@@ -15,7 +15,7 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 SOURCES = [os.path.join(B.CSRC, "kvx_attention_api.hip"), os.path.join(HERE, "attention_stub.cpp"),
            os.path.join(HERE, "attention_validate.c")]
 HEADERS = [os.path.join(B.INCLUDE, h) for h in ("kvx.h", "kvx_attention.h")] + \
-    [os.path.join(B.CSRC, "kvx_attention_launch.h")]
+    [os.path.join(B.CSRC, h) for h in ("kvx_attention_check.h", "kvx_attention_launch.h", "kvx_attention_plan.h")]
 
 
 def build() -> str:

@@ -15,7 +15,7 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 SOURCES = [os.path.join(B.CSRC, "kvx_fp4_api.hip"), os.path.join(HERE, "fp4_stub.cpp"),
            os.path.join(HERE, "fp4_validate.c")]
 HEADERS = [os.path.join(B.INCLUDE, h) for h in ("kvx.h", "kvx_attention.h", "kvx_fp4.h")] + \
-    [os.path.join(B.CSRC, h) for h in ("kvx_attention_check.h", "kvx_attention_launch.h", "kvx_fp4_launch.h")]
+    [os.path.join(B.CSRC, h) for h in ("kvx_attention_check.h", "kvx_attention_launch.h", "kvx_attention_plan.h", "kvx_fp4_launch.h")]
 
 
 def build() -> str:
