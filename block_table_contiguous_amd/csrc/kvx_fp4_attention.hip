@@ -464,8 +464,8 @@ __device__ __forceinline__ f32x16 product(Fp16, u32x4 a, u32x4 b, f32x16 c) {
 }
 
 // Many rows: 128 of them a workgroup, 32 a wavefront, and 64 slots a step, which the four wavefronts widen to 16 bits on their
-// way to LDS, 16 slots each. Scores transposed as above, with the 32x32x16 products. 2048 tokens over 32768 slots, 32 heads on 8, take 1035 us,
-// 1030 TFLOP/s: the matrix units are busy 45% of the time and the vector units 47%, which share a SIMD's issue and run side by
+// way to LDS, 16 slots each. Scores transposed as above, with the 32x32x16 products. 2048 tokens over 32768 slots, 32 heads on 8, take 1020 us,
+// 1040 TFLOP/s: the matrix units are busy 46% of the time and the vector units 52%, which share a SIMD's issue and run side by
 // side only as far as its two wavefronts are at different work.
 //   SHARED: the grid's workgroups take equal shares of the whole batch's steps (see Shares).
 template <class E, int DP, bool SHARED>

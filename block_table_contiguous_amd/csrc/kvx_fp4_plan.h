@@ -7,15 +7,17 @@
 
 namespace kvx {
 
+// Times in this file are of whole calls, the join's launch among them, queued back to back on one stream.
+//
 // A request's rows of one KV head are taken 16 or 32 at a time, by four wavefronts that take 32 slots each of every 128, or, where there
 // are more, 128 at a time, 64 slots a step, which reads a context once for up to 128 rows but widens it slower than 16-row tiles stream
-// it. 32 requests of up to 8192 slots, 32 heads on 8, dimension 128: 1 token (4 rows) takes 44 us in tiles of 16 and 58 in tiles of 32;
-// 8 tokens 68 in tiles of 32 and 107 in tiles of 128; 16 tokens, two tiles of 32, 93 and 112; 24 tokens 122 and 110. At
-// dimension 256, where a CU holds one tile of 128, 24 tokens 312 and 329 (439 unshared), 32 tokens 377 and 334.
+// it. 32 requests of up to 8192 slots, 32 heads on 8, dimension 128: 1 token (4 rows) takes 44 us in tiles of 16 and 57 in tiles of 32;
+// 8 tokens 67 in tiles of 32 and 108 in tiles of 128; 16 tokens, two tiles of 32, 93 and 115; 24 tokens 121 and 111 (at dimension 64 75
+// and 81). At dimension 256, where a CU holds one tile of 128, 24 tokens 310 and 328, 32 tokens 377 and 334.
 //
 // Where the tiles do not fill the GPU, or are uneven, the batch's steps are shared out evenly (see Shares) to as many workgroups as the
-// GPU holds, of 256 slots at least (with 512, one request of 8000 slots takes 18.1 us and not 16.1).
-constexpr int kFp4Extra = 2;  // steps that the start of a tile of few rows counts for: the decode batch takes 38.3 us, with 0 40.4
+// GPU holds, of 256 slots at least (with 512, one request of 8000 slots takes 19 us and not 17).
+constexpr int kFp4Extra = 2;  // steps that the start of a tile of few rows counts for: the decode batch takes 44 us, with 0 46
 constexpr int64_t kFp4MaxWorkgroups = (1 << 24) - 1;  // of 256 threads: a launch has fewer than 2^32
 
 struct Fp4Plan {
@@ -39,15 +41,16 @@ inline Fp4Plan plan_attention_fp4(const kvx_paged_cache& c, const kvx_batch& b, 
   if (busy < 1) busy = 1;
   const int64_t context = b.max_context_len < 0x7fffffff ? b.max_context_len : 0x7fffffff;
   // The workgroups that the registers leave room for, 1 to 4 a CU. 32 requests of up to 8192 slots, 32 heads on 8: one token of
-  // dimension 256 takes 82 us, with 768 158; 8 tokens of 128 66 us, with 768 84; one of 128 38 us, with 512 46 and with 1024 49; one of
-  // 64 34 us, with 768 36.
+  // dimension 256 takes 76 us, with 768 95; one of 128 44 us, with 512 50 and with 1024 55; one of 64 30 us, with 768 31 and with 512 34;
+  // 8 tokens of 256 149 us, with 512 159; of 128 67 us, with 768 83; of 64 44 us, with 512 51 and with 1024 54.
   const int64_t fill = p.rows == 16 ? (dim > 128 ? 512 : dim > 64 ? 768 : 1024) : dim > 128 ? 256 : few && dim <= 64 ? 768 : 512;
   int64_t shares = fill / c.num_kv_heads, most = busy * (context / 256), least = few ? busy / 4 : busy;
   if (shares > most) shares = most;
   // Tiles of 128 rows that fill the GPU, up to four times: shares take every tile of a request to be as long as its context, so only
   // where they nearly are (no prompts, no window), and the rounds come out uneven: by requests, or by a last round that is
-  // part empty. 2304 tokens over 32768 slots, 32 heads on 8, take 1240 us and not 1693; 4096, two full rounds, 2029 and not 2004; 32 chunks of
-  // up to 517 over up to 9216, 8 heads on one, 300 and not 397; a prompt of 8192 tokens 278 and not 195.
+  // part empty. 2304 tokens over 32768 slots, 32 heads on 8, take 1230 us and not 1678; 32 chunks of up to 517 over up to 9216, 8 heads on
+  // one, 300 and not 392. Shared out all the same, 4096 tokens, two full rounds, would take 2112 us and not 1974, a prompt of 8192 275 and
+  // not 195.
   const int64_t work = busy * c.num_kv_heads;
   bool uneven = work < (few ? 4 * fill : fill);
   if (!few && !uneven && work < 4 * fill && longest <= context / 4 && window >= context &&
@@ -55,8 +58,9 @@ inline Fp4Plan plan_attention_fp4(const kvx_paged_cache& c, const kvx_batch& b, 
     uneven = true;
     least = busy / 4;
   }
-  // Where rows see few slots a second launch costs more than it spares: 8 requests of 700 slots, 32 heads on 8, take 12.7 us and shared
-  // out 16.3, of 1200 slots 17.1 and 15.9; 13 requests of 5003 with a window of 256 take 13.0 and 17.1, with one of 1024 20.9 and 19.0.
+  // Where rows see few slots a second launch costs more than it spares: 8 requests of 896 slots, 32 heads on 8, take 13 us and shared
+  // out 14 to 16, of 1024 14 and 14 to 16, of 1200 17 and 15 to 16; 13 requests of 5003 with a window of 256 take 11 and 16, with one of
+  // 800 18.2 and 17.1 to 18.0, with one of 1024 20.4 and 18.2 to 19.0. One limit for both lies between what either would like.
   const bool few_slots = (context < window ? context : window) <= 896;
   p.busy = busy;
   p.shares = uneven && !few_slots && shares > least ? (int32_t)shares : 0;
